@@ -53,9 +53,10 @@
  *     capturing it (COC_ERR_CAPTURE otherwise).  The MoE all-to-all pair
  *     works only through those counters and returns COC_ERR_CAPTURE under
  *     capture.  Replays of one graph must not overlap each other.  One
- *     capture holds at most one call of this library: a second call made
+ *     capture holds at most one call of these ops: a second call made
  *     while the same capture is open (on any stream) returns
- *     COC_ERR_CAPTURE and enqueues nothing.
+ *     COC_ERR_CAPTURE and enqueues nothing.  (The row operators below are
+ *     free of all this.)
  *   - `split` is the number of m-chunks the work is pipelined over: 1
  *     (serial, no overlap), 2, 4 or 8 (CoC guide, "Usage": the split count
  *     options; the m dimension must divide by it, CoC guide "Approach" and
@@ -139,6 +140,11 @@ typedef enum coc_dtype {
     COC_F16 = 1,   /* IEEE binary16 */
     COC_BF16 = 2   /* bfloat16 */
 } coc_dtype;
+
+typedef enum coc_index {
+    COC_I32 = 0,   /* 32-bit signed ids */
+    COC_I64 = 1    /* 64-bit signed ids */
+} coc_index;
 
 typedef enum coc_quant_mode {
     COC_PER_TENSOR = 0,   /* one scale                          */
@@ -389,6 +395,156 @@ coc_status coc_matmul_all_reduce_w8a16(const void* x_f16, const int8_t* w_q, con
                                        int64_t m, int64_t n, int64_t k,
                                        int32_t split, int32_t deterministic,
                                        void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * ------------------------------------------------------------------ row operators
+ * What a training step computes between the matmul/collective ops: the layer
+ * norm in front of a column-parallel matmul, the embedding lookup, and the
+ * router and row moves around the MoE all-to-all.  Matrices are dense and
+ * row-major unless a row stride is an argument.
+ *
+ * Unlike the matmul/collective ops, these take any sizes (odd ones too; each
+ * matrix below 2^31 elements and 2^26 rows) and any element-aligned pointer.
+ * All their work goes to `stream` as plain kernel launches: any number of
+ * them may be captured into one graph, replayed, and called from several
+ * threads; a workspace belongs to one call at a time.  Sums, statistics and
+ * gates are binary32; results are rounded once, to nearest even.  The bits
+ * of every result depend on the inputs and sizes alone (no floating-point
+ * atomics).  Outputs must not overlap inputs or each other.  A NULL pointer
+ * is refused (COC_ERR_NULL) unless the argument is called optional.
+ */
+
+/*
+ * Layer norm over rows of n elements (1 <= n <= 32768):
+ *
+ *   h    = x, or round_dt(x + residual) where residual is given
+ *   mean = sum(h) / n,   rstd = 1 / sqrt(sum((h - mean)^2) / n + eps)
+ *   y    = round_dt((h - mean) * rstd * gamma + beta)
+ *
+ * x, y, residual, sum_out: rows x n of `dt`; gamma, beta: n of `param_dt`
+ * (dt or COC_F32); mean, rstd: rows, binary32.  residual is optional; where it
+ * is given sum_out receives h (the next residual, and the x of the backward
+ * pass), otherwise sum_out is not used.  beta is optional.
+ */
+coc_status coc_layer_norm(const void* x, const void* residual, const void* gamma, const void* beta, void* y,
+                          void* sum_out, float* mean, float* rstd, int64_t rows, int64_t n, float eps,
+                          coc_dtype dt, coc_dtype param_dt, hipStream_t stream);
+
+/*
+ * Its backward pass, x being the h that was normalised.  With
+ * xh = (x - mean) * rstd and g = dy * gamma:
+ *
+ *   dx     = round_dt(rstd * (g - sum(g) / n - xh * sum(g * xh) / n) + dsum)
+ *   dgamma = round(sum over rows of dy * xh),   dbeta = round(sum over rows of dy)
+ *
+ * dsum (optional, rows x n): the gradient that reaches the sum h by the
+ * residual branch.  dgamma, dbeta: n of param_dt, overwritten (zeros where
+ * rows is 0); dbeta is optional.  ws: at least
+ * coc_layer_norm_backward_workspace_bytes(rows, n), 4-byte aligned.
+ */
+size_t coc_layer_norm_backward_workspace_bytes(int64_t rows, int64_t n);
+coc_status coc_layer_norm_backward(const void* dy, const void* x, const void* gamma, const float* mean,
+                                   const float* rstd, const void* dsum, void* dx, void* dgamma, void* dbeta,
+                                   int64_t rows, int64_t n, coc_dtype dt, coc_dtype param_dt, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Embedding lookup of one tensor-parallel rank's vocabulary shard, ids
+ * [start, start + vocab):
+ *
+ *   y[t] = round_dt(scale * table[ids[t] - start]),  zeros where ids[t] is outside the shard
+ *
+ * (the ranks' results add up to the whole lookup).  ids: tokens of `id_type`,
+ * any values; table: vocab x n; y: tokens x n; start >= 0.
+ */
+coc_status coc_embedding(const void* ids, coc_index id_type, const void* table, void* y, int64_t tokens,
+                         int64_t vocab, int64_t n, int64_t start, float scale, coc_dtype dt, hipStream_t stream);
+
+/*
+ * Its gradient:
+ *
+ *   grad[v] = round(scale * sum of dy[t] over the tokens t with ids[t] == start + v  (+ grad[v] if accumulate))
+ *
+ * the sum in binary32.  The tokens are sorted by their row first, so every
+ * row of the gradient is written once and in an order fixed by the ids; rows
+ * without tokens become zeros (accumulate: stay as they are).  dy: tokens x n
+ * of `dt`; grad: vocab x n of `grad_dt` (dt or COC_F32).  ws: at least
+ * coc_embedding_grad_workspace_bytes(tokens, n), 8-byte aligned.
+ */
+size_t coc_embedding_grad_workspace_bytes(int64_t tokens, int64_t n);
+coc_status coc_embedding_grad(const void* ids, coc_index id_type, const void* dy, void* grad, int64_t tokens,
+                              int64_t vocab, int64_t n, int64_t start, float scale, int32_t accumulate,
+                              coc_dtype dt, coc_dtype grad_dt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * MoE router of one rank's tokens (the routing that the all-to-all pair above
+ * takes as given).  For each token, over `experts` (1..512) experts:
+ *
+ *   p           = softmax(logits[t])
+ *   ids[t][j]   = the j-th largest logit's expert, j < topk (<= 16); ties: the lowest index
+ *   gates[t][j] = p of that expert, divided by their sum over j if renormalize
+ *   counts[q][e]    = choices of expert e by the tokens of sequence piece q,
+ *                     tokens [tokens*q/pieces, tokens*(q+1)/pieces)
+ *   positions[t][j] = the choice's row among all rows this rank sends, ordered by
+ *                     destination rank (expert / (experts/world)), piece, expert, token:
+ *                     destination r's rows are one block in the order that
+ *                     coc_alltoall_grouped_matmul expects of its x_own / peer_bufs
+ *   prob_sums[e]    = sum of p over the tokens
+ *   loss        = coef * experts / (topk * N^2) * sum_e counts[.][e] * prob_sums[e]
+ *
+ * N = *valid: the tokens that take part, those whose mask is not 0 (mask
+ * optional: all) and that have a logit above -inf.  Other tokens, and the
+ * choices a token cannot make because fewer than topk of its logits are above
+ * -inf, get id -1, gate 0, position -1 and count nowhere.  N == 0: loss 0.  A
+ * NaN logit of a token that takes part counts as the largest and makes its
+ * probabilities NaN; masked tokens' logits are never used.
+ *
+ * logits: tokens rows of `ld` elements, the first `experts` used; mask:
+ * tokens bytes; ids, gates, positions: tokens x topk; counts: pieces x
+ * experts; pieces in [1, COC_MAX_SPLIT]; world divides experts.  ws: at least
+ * coc_moe_router_workspace_bytes(tokens, experts, pieces), 4-byte aligned.
+ */
+size_t coc_moe_router_workspace_bytes(int64_t tokens, int32_t experts, int32_t pieces);
+coc_status coc_moe_router(const void* logits, int64_t ld, const uint8_t* mask, int32_t* ids, float* gates,
+                          int32_t* positions, int64_t* counts, float* prob_sums, float* loss, int64_t* valid,
+                          int64_t tokens, int32_t experts, int32_t topk, int32_t pieces, int32_t world, float coef,
+                          int32_t renormalize, coc_dtype dt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Its gradient by the logits, given dgates (tokens x topk, optional) and
+ * dloss (one binary32 value on the device, optional), with the forward's ids,
+ * gates, counts and valid; the counts are constants.  Tokens that take no
+ * part get zeros.  dlogits: tokens rows of `ld_out` elements, of which the
+ * first `experts` are written.
+ */
+coc_status coc_moe_router_backward(const void* logits, int64_t ld, const uint8_t* mask, const int32_t* ids,
+                                   const float* gates, const int64_t* counts, const int64_t* valid,
+                                   const float* dgates, const float* dloss, void* dlogits, int64_t ld_out,
+                                   int64_t tokens, int32_t experts, int32_t topk, int32_t pieces, float coef,
+                                   int32_t renormalize, coc_dtype dt, hipStream_t stream);
+
+/*
+ * Row moves between the tokens and the send rows of coc_moe_router's
+ * positions (tokens x topk, topk <= 16; an entry outside [0, rows) stands for
+ * no row and is skipped; no two entries name the same row).
+ *
+ *   coc_moe_permute:          out[positions[t][j]] = x[t]                           (bit copy)
+ *   coc_moe_combine:          y[t] = round_dt(sum_j gates[t][j] * h[positions[t][j]]), added in order of j
+ *   coc_moe_combine_backward: dh[positions[t][j]] = round_dt(gates[t][j] * dy[t]),
+ *                             dgates[t][j] = sum(dy[t] * h[positions[t][j]]), 0 without a row
+ *
+ * x, y, dy: tokens x n; out, h, dh: rows x n; gates, dgates: tokens x topk,
+ * binary32.  combine's gates are optional (NULL: all 1), which makes it the
+ * gradient of permute.  Rows of out and dh that no entry names are not
+ * written; a token without rows gets zeros in y.
+ */
+coc_status coc_moe_permute(const void* x, const int32_t* positions, void* out, int64_t tokens, int64_t rows,
+                           int64_t n, int32_t topk, coc_dtype dt, hipStream_t stream);
+coc_status coc_moe_combine(const void* h, const int32_t* positions, const float* gates, void* y, int64_t tokens,
+                           int64_t rows, int64_t n, int32_t topk, coc_dtype dt, hipStream_t stream);
+coc_status coc_moe_combine_backward(const void* dy, const void* h, const int32_t* positions, const float* gates,
+                                    void* dh, float* dgates, int64_t tokens, int64_t rows, int64_t n, int32_t topk,
+                                    coc_dtype dt, hipStream_t stream);
 
 /* Workspace bytes an op (a coc_op value) needs at these sizes (0 when it needs none).
  * dt is ignored for COC_OP_MATMUL_ALL_REDUCE_W8A16.  Returns 0 for invalid

@@ -29,3 +29,15 @@ from .coc import (  # noqa: F401
     profile_records,
     diag_mfma_loop,
 )
+from .row_ops import (  # noqa: F401
+    Routing,
+    layer_norm,
+    layer_norm_backward,
+    embedding,
+    embedding_grad,
+    moe_router,
+    moe_router_backward,
+    moe_permute,
+    moe_combine,
+    moe_combine_backward,
+)

@@ -38,6 +38,10 @@ EXPORTS = (
     "coc_grouped_matmul_alltoall", "coc_workspace_bytes", "coc_status_string",
     "coc_last_error", "coc_check_waits", "coc_plan", "coc_profile_enable", "coc_profile_read",
     "coc_profile_records", "coc_profile_stamps", "coc_profile_stamp_count", "coc_diag_mfma_loop",
+    "coc_layer_norm", "coc_layer_norm_backward", "coc_layer_norm_backward_workspace_bytes",
+    "coc_embedding", "coc_embedding_grad", "coc_embedding_grad_workspace_bytes",
+    "coc_moe_router", "coc_moe_router_backward", "coc_moe_router_workspace_bytes",
+    "coc_moe_permute", "coc_moe_combine", "coc_moe_combine_backward",
 )
 
 
@@ -117,8 +121,33 @@ def lib() -> ctypes.CDLL:
     dp = ctypes.POINTER(ctypes.c_double)
     L.coc_profile_records.argtypes = [ctypes.POINTER(_i32), dp, dp, dp, _i32, ctypes.POINTER(_i32)]
     L.coc_profile_records.restype = _i32
+    _declare_row_ops(L)
     _lib = L
     return L
+
+
+def _declare_row_ops(L) -> None:
+    f32 = ctypes.c_float
+    for name, args in {
+        "coc_layer_norm": [_vp] * 8 + [_i64, _i64, f32, _i32, _i32, _vp],
+        "coc_layer_norm_backward": [_vp] * 9 + [_i64, _i64, _i32, _i32, _vp, _sz, _vp],
+        "coc_embedding": [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _i64, f32, _i32, _vp],
+        "coc_embedding_grad": [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _i64, f32, _i32, _i32, _i32, _vp, _sz, _vp],
+        "coc_moe_router": [_vp, _i64] + [_vp] * 8 + [_i64, _i32, _i32, _i32, _i32, f32, _i32, _i32, _vp, _sz, _vp],
+        "coc_moe_router_backward": [_vp, _i64] + [_vp] * 8 + [_i64, _i64, _i32, _i32, _i32, f32, _i32, _i32, _vp],
+        "coc_moe_permute": [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp],
+        "coc_moe_combine": [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp],
+        "coc_moe_combine_backward": [_vp] * 6 + [_i64, _i64, _i64, _i32, _i32, _vp],
+    }.items():
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = _i32
+    for name, args in {
+        "coc_layer_norm_backward_workspace_bytes": [_i64, _i64],
+        "coc_embedding_grad_workspace_bytes": [_i64, _i64],
+        "coc_moe_router_workspace_bytes": [_i64, _i32, _i32],
+    }.items():
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = _sz
 
 
 def _check(status: int) -> None:

@@ -23,8 +23,10 @@ ARCH = "gfx950"
 
 # coc_api.cpp holds host code and one device array (the allocation-free entry
 # point's scratch memory), so it takes the device pass as well; diag.hip holds
-# the MFMA-rate diagnostic.
-DEVICE_SOURCES = ["kernels.hip", "coc_api.cpp", "diag.hip"]
+# the MFMA-rate diagnostic; the last four hold the row operators with their
+# entry points.
+DEVICE_SOURCES = ["kernels.hip", "coc_api.cpp", "diag.hip", "layer_norm.hip", "embedding.hip", "moe_router.hip",
+                  "moe_rows.hip"]
 HOST_SOURCES = ["coc_plan.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{HERE}"]

@@ -1,0 +1,199 @@
+// Shared by the row operators (layer norm, embedding, MoE router, MoE row
+// moves): argument checks on the host, and on the device 16-byte row vectors
+// of any alignment, conversions, and reductions over lanes and workgroups.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "coc.h"
+#include "coc_internal.h"
+
+namespace coc {
+
+// ------------------------------------------------------------------ host checks
+// One pointer argument.  The row operators take any element-aligned address:
+// their 16-byte loads and stores need no more (see load_vec).
+struct Arg {
+    const void* p;
+    int64_t bytes;   // 0: not read or written, may be NULL
+    int32_t align;   // element size
+    bool out;
+    const char* name;
+};
+
+inline coc_status check_args(const Arg* a, int count) {
+    for (int i = 0; i < count; ++i) {
+        if (a[i].bytes <= 0) continue;
+        if (!a[i].p) return fail(COC_ERR_NULL, "%s is NULL", a[i].name);
+        if ((uintptr_t)a[i].p % (uintptr_t)a[i].align != 0)
+            return fail(COC_ERR_ALIGN, "%s is not %d-byte aligned", a[i].name, a[i].align);
+    }
+    for (int i = 0; i < count; ++i) {
+        if (!a[i].out || a[i].bytes <= 0) continue;
+        for (int j = 0; j < count; ++j) {
+            if (j == i || a[j].bytes <= 0 || (a[j].out && j < i)) continue;
+            const uintptr_t lo = (uintptr_t)a[i].p, lo2 = (uintptr_t)a[j].p;
+            if (lo < lo2 + (uintptr_t)a[j].bytes && lo2 < lo + (uintptr_t)a[i].bytes)
+                return fail(COC_ERR_ALIAS, "%s overlaps %s", a[i].name, a[j].name);
+        }
+    }
+    return COC_OK;
+}
+
+// rows x cols of a matrix within the library's limits.  The row limit keeps
+// every launch below 2^32 threads (at most 64 a row where a row is short).
+inline coc_status check_matrix(int64_t rows, int64_t cols, const char* what) {
+    const int64_t lim = int64_t(1) << 31;
+    if (rows < 0 || cols < 0) return fail(COC_ERR_SHAPE, "%s has a negative size", what);
+    if (rows >= lim || cols >= lim || rows * cols >= lim)
+        return fail(COC_ERR_SHAPE, "%s has 2^31 or more elements", what);
+    if (rows >= int64_t(1) << 26) return fail(COC_ERR_SHAPE, "%s has 2^26 or more rows", what);
+    return COC_OK;
+}
+
+inline coc_status launched(const char* what) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(COC_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
+    return COC_OK;
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// ------------------------------------------------------------------ device: types and vectors
+typedef _Float16 f16_t;
+typedef __bf16 bf16_t;
+
+// Elements of T in 16 bytes.
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// 16 bytes at an address aligned to T only.  Global memory takes 16-byte
+// accesses of any alignment in the unaligned access mode that the HSA ABI
+// runs in, so rows of odd length need no path of their own.
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Packed {
+    T e[kVec<T>];
+};
+
+// Row elements [c, c + kVec) as binary32; those at or past n become 0.
+template <class T>
+__device__ __forceinline__ void load_vec(const T* row, int c, int n, float* f) {
+    if (c + kVec<T> <= n) {
+        Packed<T> p;
+        __builtin_memcpy(&p, row + c, 16);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) f[i] = (float)p.e[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) f[i] = c + i < n ? (float)row[c + i] : 0.0f;
+    }
+}
+
+// The same without the conversion (kept packed until it is used).
+template <class T>
+__device__ __forceinline__ void load_raw(const T* row, int c, int n, Packed<T>* p) {
+    if (c + kVec<T> <= n) {
+        __builtin_memcpy(p, row + c, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) p->e[i] = c + i < n ? row[c + i] : (T)0.0f;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_raw(T* row, int c, int n, const Packed<T>& p) {
+    if (c + kVec<T> <= n) {
+        __builtin_memcpy(row + c, &p, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i)
+            if (c + i < n) row[c + i] = p.e[i];
+    }
+}
+
+// Each element rounded once, to nearest even.
+template <class T>
+__device__ __forceinline__ void store_vec(T* row, int c, int n, const float* f) {
+    if (c + kVec<T> <= n) {
+        Packed<T> p;
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) p.e[i] = (T)f[i];
+        __builtin_memcpy(row + c, &p, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i)
+            if (c + i < n) row[c + i] = (T)f[i];
+    }
+}
+
+// kVec<T> elements of a parameter or sum vector whose type U may be wider than T.
+template <int N, class U>
+__device__ __forceinline__ void load_n(const U* v, int c, int n, float* f) {
+    if (c + N <= n) {
+        struct __attribute__((packed, aligned(sizeof(U)))) { U e[N]; } p;
+        __builtin_memcpy(&p, v + c, sizeof(p));
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = (float)p.e[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = c + i < n ? (float)v[c + i] : 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------ device: reductions
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+constexpr int kDppXor1 = 0xB1;         // quad_perm [1, 0, 3, 2]
+constexpr int kDppXor2 = 0x4E;         // quad_perm [2, 3, 0, 1]
+constexpr int kDppHalfMirror = 0x141;  // within 8 lanes: the other quad
+constexpr int kDppMirror = 0x140;      // within 16 lanes: the other 8
+
+// Sum over aligned groups of LANES lanes, the same bits in each of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (LANES >= 2) v += dpp_f<kDppXor1>(v);
+    if constexpr (LANES >= 4) v += dpp_f<kDppXor2>(v);
+    if constexpr (LANES >= 8) v += dpp_f<kDppHalfMirror>(v);
+    if constexpr (LANES >= 16) v += dpp_f<kDppMirror>(v);
+    if constexpr (LANES >= 32) v += __shfl_xor(v, 16);
+    if constexpr (LANES >= 64) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// Largest value over aligned groups of LANES lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    if constexpr (LANES >= 2) v = max(v, dpp_u<kDppXor1>(v));
+    if constexpr (LANES >= 4) v = max(v, dpp_u<kDppXor2>(v));
+    if constexpr (LANES >= 8) v = max(v, dpp_u<kDppHalfMirror>(v));
+    if constexpr (LANES >= 16) v = max(v, dpp_u<kDppMirror>(v));
+    if constexpr (LANES >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    if constexpr (LANES >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    return v;
+}
+
+// Sum over a workgroup of THREADS threads, in a fixed order; `buf` holds a
+// float per wave.  Callers that reuse a buf have a barrier between.
+template <int THREADS>
+__device__ __forceinline__ float group_sum(float v, float* buf) {
+    v = lanes_sum<64>(v);
+    if constexpr (THREADS > 64) {
+        if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = buf[0];
+#pragma unroll
+        for (int w = 1; w < THREADS / 64; ++w) v += buf[w];
+    }
+    return v;
+}
+
+}  // namespace coc
