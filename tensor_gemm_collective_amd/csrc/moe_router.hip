@@ -8,289 +8,612 @@ namespace {
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopk = 16;
 constexpr int kPerLane = 8;     // experts a lane holds
-constexpr int kThreads = 512;
-constexpr int kChunk = 256;     // tokens a workgroup ranks at a time
+constexpr int kThreads = 256;
+constexpr int kAlone = 1024;
+constexpr int kChunk = 256;         // tokens a workgroup ranks at a time
 constexpr int kWords = kChunk / 32;
-constexpr int kMostBlocks = 256;
+constexpr int kMostBlocks = 1024;   // runs, and workgroups
+constexpr int kLeastRun = 32;       // tokens
 
-// exp(x) for x <= 0.  x log2(e) is split into its rounded product and what
-// that rounding lost; exp2 takes the first, the second enters to first order.
-__device__ __forceinline__ float exp_neg(float x) {
-    constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147180559945309417f;
-    x = fmaxf(x, -200.0f);   // exp is 0 there; -inf would make the correction NaN
-    const float hi = x * kLog2e;
-    const float lo = fmaf(x, kLog2e, -hi) + x * kLog2eLow;
-    const float e = __builtin_amdgcn_exp2f(hi);
-    return fmaf(e * kLn2, lo, e);
-}
+constexpr float kLog2e = 1.44269504088896340736f;
 
-// A lane's logits as binary32 (-inf past the last expert).  Lane l of a
-// token's LG lanes holds experts [8 l, 8 l + 8).
+// A choice's key: the logit's bits in unsigned order above 0xffff - expert, so
+// that keys differ and the largest is the largest logit's lowest expert.  16
+// bits hold a 16-bit logit's order, 32 a binary32's.  Every NaN orders above
+// +inf, -0 as +0; a key at or below kNone stands for no choice (-inf, or 0
+// for what is not there or has been taken).
 template <class T>
-__device__ __forceinline__ void load_logits(const T* row, int e0, int experts, float* x) {
-    if (e0 + kPerLane <= experts) {
-        load_n<kPerLane>(row, e0, experts, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) x[i] = e0 + i < experts ? (float)row[e0 + i] : -INFINITY;
+struct Order {
+    typedef uint32_t Key;
+    static constexpr uint32_t kNegInf = std::is_same_v<T, bf16_t> ? 0x007fu : 0x03ffu;
+    // x holds a T exactly: its bits are the upper half of a bfloat16's binary32
+    __device__ static uint32_t high(float x) {
+        if constexpr (std::is_same_v<T, bf16_t>) return __float_as_uint(x);
+        return (uint32_t)__builtin_bit_cast(uint16_t, (T)x) << 16;
     }
+    __device__ static float value(uint32_t b) { return (float)__builtin_bit_cast(T, (uint16_t)(b >> 16)); }
+    __device__ static Key key(uint32_t o, uint32_t e) { return (o & 0xffff0000u) | (0xffffu - e); }
+    __device__ static uint32_t order(Key k) { return k & 0xffff0000u; }
+};
+template <>
+struct Order<float> {
+    typedef uint64_t Key;
+    static constexpr uint32_t kNegInf = 0x007fffffu;
+    __device__ static uint32_t high(float x) { return __float_as_uint(x); }
+    __device__ static float value(uint32_t b) { return __uint_as_float(b); }
+    __device__ static Key key(uint32_t o, uint32_t e) { return (uint64_t)o << 16 | (0xffffu - e); }
+    __device__ static uint32_t order(Key k) { return (uint32_t)(k >> 16); }
+};
+template <class T>
+using Key = typename Order<T>::Key;
+template <class T>
+constexpr Key<T> kNone = ((Key<T>)Order<T>::kNegInf << 16) | 0xffffu;
+
+template <class T>
+__device__ __forceinline__ int key_expert(Key<T> k) { return 0xffff - (int)(k & 0xffffu); }
+template <class T>
+__device__ __forceinline__ float key_logit(Key<T> k) {
+    const uint32_t o = Order<T>::order(k);
+    return Order<T>::value(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// Unsigned order of logits: larger key, larger logit; every NaN above +inf,
-// -inf and lower is key 0x007fffff, nothing (taken) is 0.
-__device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x) return 0xffffffffu;
-    const uint32_t b = __float_as_uint(x + 0.0f);   // -0 orders as +0
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-constexpr uint32_t kKeyNegInf = 0x007fffffu;
-
-// Softmax of a token over its LG lanes: x becomes exp(x - max).  Returns
-// whether the token takes part (its mask is set and a logit is above -inf).
-template <int LG>
-__device__ __forceinline__ bool softmax_parts(float* x, const uint32_t* key, bool live, float* total) {
-    uint32_t mk = 0;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) mk = max(mk, key[i]);
-    mk = lanes_max<LG>(mk);
-    live = live && mk > kKeyNegInf;
-    const float top = __uint_as_float(mk & 0x80000000u ? mk ^ 0x80000000u : ~mk);   // NaN stays NaN
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-        x[i] = !live ? 0.0f : x[i] == -INFINITY ? (top != top || top == INFINITY ? top - top : 0.0f)
-                            : (x[i] != x[i] || top - top != 0.0f ? x[i] - top : exp_neg(x[i] - top));
-        s += x[i];
-    }
-    *total = lanes_sum<LG>(s);
-    return live;
-}
-
-// Where the parts of a launch are: the tokens of piece p are
-// [tokens p / pieces, tokens (p + 1) / pieces), cut into `per` runs for as
-// many workgroups, so that no workgroup's run crosses a piece.
-struct Runs {
-    int64_t tokens;
-    int32_t pieces, per;
-    __host__ __device__ int64_t piece_begin(int64_t p) const { return tokens * p / pieces; }
-    __host__ __device__ int64_t begin(int b) const {
-        const int64_t p = b / per, i = b % per, t0 = piece_begin(p);
-        return t0 + (piece_begin(p + 1) - t0) * i / per;
-    }
-    __host__ __device__ int64_t end(int b) const {
-        const int64_t p = b / per, i = b % per, t0 = piece_begin(p);
-        return t0 + (piece_begin(p + 1) - t0) * (i + 1) / per;
+// 8 of a lane's logits, kept as stored until they are used.
+template <class T>
+struct Logits {
+    static constexpr int kWords = kPerLane * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return (float)__builtin_bit_cast(T, (uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu));
     }
 };
 
-// Workgroup b routes its run.  Softmax and selection: LG lanes a token, k
-// rounds of "largest key, lowest expert".  A chunk's choices go into a bit per
-// (expert, token) in LDS; a choice's rank among its expert's is then the
-// number of bits before it, whatever order the waves ran in.  Leaves each
-// position's rank within the run, the run's counts (hist), probability sums
-// and number of tokens that take part.
-template <class T, int LG>
-__global__ __launch_bounds__(kThreads) void route_runs(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
-                                                       int experts, int topk, int renormalize, int32_t* ids,
-                                                       float* gates, int32_t* positions, int32_t* hist, float* psum,
-                                                       int32_t* nvalid) {
-    constexpr int GROUPS = kThreads / LG;
-    extern __shared__ uint32_t lds[];
-    uint32_t* bits = lds;                                  // experts x kWords
-    int32_t* seen = (int32_t*)(bits + experts * kWords);   // experts: choices of earlier chunks
-    float* under = (float*)(seen + experts);               // kChunk: 1 / the gates' denominator
-    int16_t* cid = (int16_t*)(under + kChunk);             // kChunk x topk
-    float* cval = (float*)(cid + kChunk * kMaxTopk);       // kChunk x topk
-    __shared__ int32_t taken;
-    const int group = threadIdx.x / LG, lane = threadIdx.x % LG;
-    const int e0 = lane * kPerLane;
-    const int64_t t0 = runs.begin(blockIdx.x), t1 = runs.end(blockIdx.x);
-    for (int e = threadIdx.x; e < experts; e += kThreads) seen[e] = 0;
-    if (threadIdx.x == 0) taken = 0;
-    float ps[kPerLane];
+// Experts [e0, e0 + 8) of a row; -inf past the last one.  EIGHTS: their number
+// is a multiple of 8.
+template <bool EIGHTS, class T>
+__device__ __forceinline__ void load_logits(const T* row, int e0, int experts, Logits<T>* l) {
+    constexpr uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : std::is_same_v<T, bf16_t> ? 0xff80ff80u : 0xfc00fc00u;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) ps[i] = 0.0f;
-    int mine = 0;
-    for (int64_t c0 = t0; c0 < t1; c0 += kChunk) {
-        const int len = (int)min((int64_t)kChunk, t1 - c0);
-        for (int i = threadIdx.x; i < experts * kWords; i += kThreads) bits[i] = 0;
-        __syncthreads();
-        for (int tl = group; tl < len; tl += GROUPS) {
-            const int64_t t = c0 + tl;
-            float x[kPerLane], total;
-            uint32_t key[kPerLane];
-            load_logits(logits + t * ld, e0, experts, x);
-            bool live = !mask || mask[t] != 0;
+    for (int i = 0; i < Logits<T>::kWords; ++i) l->w[i] = ninf;
+    if (e0 + kPerLane <= experts) {
+        __builtin_memcpy(l->w, row + e0, sizeof(l->w));
+    } else if (!EIGHTS && e0 < experts) {
+        for (int i = 0; i < experts - e0; ++i) {
+            uint32_t v = 0;
+            __builtin_memcpy(&v, row + e0 + i, sizeof(T));
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i) key[i] = e0 + i < experts ? order_key(x[i]) : 0;
-            live = softmax_parts<LG>(x, key, live, &total);
-            const float inv = live ? 1.0f / total : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) ps[i] += live ? x[i] * inv : 0.0f;
-            if (lane == 0) mine += live;
-            float chosen = 0.0f;
-            for (int j = 0; j < topk; ++j) {
-                uint32_t best = 0;
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i) best = max(best, key[i]);
-                best = lanes_max<LG>(best);
-                const bool any = live && best > kKeyNegInf;
-                // the lowest expert with that key
-                uint32_t at = 0;   // 0xffff - expert, so the lowest is the largest
-                float v = 0.0f;
-#pragma unroll
-                for (int i = kPerLane - 1; i >= 0; --i)
-                    if (key[i] == best) {
-                        at = 0xffffu - (uint32_t)(e0 + i);
-                        v = x[i];
-                    }
-                const uint32_t win = lanes_max<LG>(at);
-                const int e = any ? (int)(0xffffu - win) : -1;
-                const bool owner = any && at == win && at != 0;
-                if (owner) {
-                    cval[tl * topk + j] = v;
-                    atomicOr(&bits[e * kWords + (tl >> 5)], 1u << (tl & 31));
+            for (int q = 0; q < Logits<T>::kWords; ++q) {   // no indexed registers
+                if constexpr (sizeof(T) == 4) {
+                    if (q == i) l->w[q] = v;
+                } else if (q == i >> 1) {
+                    l->w[q] = i & 1 ? (l->w[q] & 0xffffu) | v << 16 : (l->w[q] & 0xffff0000u) | v;
                 }
-                if (lane == 0) {
-                    cid[tl * topk + j] = (int16_t)e;
-                    if (!any) cval[tl * topk + j] = 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i)
-                    if (e0 + i == e) key[i] = 0;
-                chosen += lanes_sum<LG>(owner ? v : 0.0f);
             }
-            if (lane == 0) under[tl] = renormalize ? chosen : total;
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < len * topk; i += kThreads) {
-            const int tl = i / topk;
-            const int e = cid[i];
-            int rank = -1;
-            if (e >= 0) {
-                rank = seen[e];
-                for (int w = 0; w < (tl >> 5); ++w) rank += __popc(bits[e * kWords + w]);
-                rank += __popc(bits[e * kWords + (tl >> 5)] & ((1u << (tl & 31)) - 1u));
-            }
-            const int64_t o = c0 * topk + i;
-            ids[o] = e;
-            gates[o] = e >= 0 ? cval[i] / under[tl] : 0.0f;
-            positions[o] = rank;
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < experts; e += kThreads) {
-            int n = seen[e];
-            for (int w = 0; w < kWords; ++w) n += __popc(bits[e * kWords + w]);
-            seen[e] = n;
-        }
-        __syncthreads();
     }
-    if (lane == 0 && mine) atomicAdd(&taken, mine);
-    // probability sums: a wave's groups by shuffles, the waves in order
-    float* wsum = (float*)bits;   // kThreads / 64 x experts: at most as large as bits
+}
+
+template <class T>
+__device__ __forceinline__ void make_keys(const float* x, int e0, int experts, Key<T>* key) {
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kPerLane; i += 2) nan |= __builtin_isunordered(x[i], x[i + 1]);
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-        float v = ps[i];
-#pragma unroll
-        for (int d = LG; d < 64; d <<= 1) v += __shfl_xor(v, d);
-        ps[i] = v;
+        const uint32_t b = Order<T>::high(x[i] + 0.0f);
+        key[i] = Order<T>::key(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), e0 + i);
     }
+    if (__any(nan)) {
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (x[i] != x[i]) key[i] = Order<T>::key(0xffffffffu, e0 + i);
+    }
+    if (e0 + kPerLane > experts) {
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (e0 + i >= experts) key[i] = 0;
+    }
+}
+
+// A lane's keys from the largest down (19 exchanges, odd-even merge).
+template <class K>
+__device__ __forceinline__ void sort_keys(K* k) {
+    auto ce = [&](int a, int b) {
+        const K hi = max(k[a], k[b]), lo = min(k[a], k[b]);
+        k[a] = hi;
+        k[b] = lo;
+    };
+    ce(0, 1); ce(2, 3); ce(4, 5); ce(6, 7);
+    ce(0, 2); ce(1, 3); ce(4, 6); ce(5, 7);
+    ce(1, 2); ce(5, 6);
+    ce(0, 4); ce(1, 5); ce(2, 6); ce(3, 7);
+    ce(2, 4); ce(3, 5);
+    ce(1, 2); ce(3, 4); ce(5, 6);
+}
+static_assert(kPerLane == 8, "sort_keys orders 8 keys");
+
+// exp(x - top) is 2^(x log2(e) - c) with c = top log2(e) rounded: what that
+// rounding does is common to a token's experts and leaves the quotients.  Past
+// kHuge, where the product could overflow, the difference is taken first.
+constexpr float kHuge = 1e37f;
+__device__ __forceinline__ float exp_below(float x, float top) {
+    const bool huge = fabsf(top) > kHuge;
+    return __builtin_amdgcn_exp2f(huge ? (x - top) * kLog2e : fmaf(x, kLog2e, -(top * kLog2e)));
+}
+
+// x becomes exp(x - top).  Returns the factor that makes them
+// probabilities: 0 for a token that takes no part, NaN where the largest logit
+// is not finite.
+template <int LG>
+__device__ __forceinline__ float softmax_parts(float* x, float top, bool live) {
+    float c = top * kLog2e;
+    if (__any(!(fabsf(top) <= kHuge))) {
+        if (!(fabsf(top) < INFINITY)) {   // nothing may become NaN in a token that takes no part
+            c = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) x[i] = -INFINITY;
+        } else if (fabsf(top) > kHuge) {
+            c = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) x[i] -= top;
+        }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], kLog2e, -c));
+        s += x[i];
+    }
+    s = lanes_sum<LG>(s);
+    return live ? 1.0f / s + (top - top) : 0.0f;
+}
+
+// The tokens of piece p are [tokens p / pieces, tokens (p + 1) / pieces), cut
+// into `per` runs of `len` for as many workgroups (the last ones shorter or
+// empty), so that no run crosses a piece.
+struct Runs {
+    int32_t tokens, pieces, per, len;
+    __host__ __device__ int32_t piece_begin(int p) const { return (int32_t)((uint32_t)tokens * p / pieces); }
+    __host__ __device__ int32_t blocks() const { return pieces * per; }
+    __device__ void run(int b, int32_t* t0, int32_t* t1) const {
+        const int p = b / per, end = piece_begin(p + 1);
+        *t0 = min(piece_begin(p) + (b - p * per) * len, end);
+        *t1 = min(*t0 + len, end);
+    }
+};
+
+// What the router writes, and its workspace.
+struct RouterOut {
+    int32_t* ids;
+    float* gates;
+    int32_t* positions;
+    int64_t* counts;
+    float* prob_sums;
+    float* loss;
+    int64_t* valid;
+    int32_t* hist;      // experts x blocks: a run's choices
+    int32_t* base;      // blocks x experts: those of the piece's earlier runs
+    float* psum;        // experts x blocks
+    int32_t* nvalid;    // blocks
+};
+
+// First rows.  Rows are ordered by destination, piece, expert; entry i of that
+// order is counts[piece][expert] of slot(i).
+__device__ __forceinline__ void slot(int i, int pieces, int local, int* piece, int* expert) {
+    const int dest = i / (pieces * local), in = i % (pieces * local);
+    *piece = in / local;
+    *expert = dest * local + in % local;
+}
+
+// The rows before each entry: THREADS threads scan runs of entries; each calls
+// put(piece, expert, rows before).  `buf` holds a value per wave.
+template <int THREADS, class Get, class Put>
+__device__ __forceinline__ void first_rows(int entries, int pieces, int local, int32_t* buf, Get&& get, Put&& put) {
+    const int each = (entries + THREADS - 1) / THREADS;
+    const int i0 = threadIdx.x * each, lane = threadIdx.x & 63;
+    int32_t sum = 0;
+    for (int i = i0; i < min(i0 + each, entries); ++i) {
+        int p, e;
+        slot(i, pieces, local, &p, &e);
+        sum += get(p, e);
+    }
+    int32_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t up = __shfl_up(inc, d);
+        if (lane >= d) inc += up;
+    }
+    if (lane == 63) buf[threadIdx.x >> 6] = inc;
     __syncthreads();
+    int32_t row = inc - sum;
+    for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) row += buf[w];
+    for (int i = i0; i < min(i0 + each, entries); ++i) {
+        int p, e;
+        slot(i, pieces, local, &p, &e);
+        put(p, e, row);
+        row += get(p, e);
+    }
+}
+
+__device__ __forceinline__ float loss_term(float count, float prob_sum, float n) { return count / n * (prob_sum / n); }
+
+// One token over its LG lanes, lane l holding experts [8 l, 8 l + 8).  The lane
+// orders its keys, and each of the topk rounds takes the largest of the lanes'
+// first keys and moves the list it came from up by one.  Lane 0 writes the
+// chosen keys (0: none), the largest logit and the gates' factor; ps collects
+// the probabilities.  Returns whether the token takes part.
+template <class T, int LG>
+__device__ __forceinline__ bool route_token(const Logits<T>& l, bool take, int lane, int experts, int topk,
+                                            int renormalize, float* ps, Key<T>* ckey, float* topv, float* factor) {
+    typedef Key<T> K;
+    K key[kPerLane];
+    float x[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) x[i] = l.get(i);
+    make_keys<T>(x, lane * kPerLane, experts, key);
+    sort_keys(key);
+    K best = lanes_max<LG>(key[0]);
+    const float top = key_logit<T>(best);
+    const bool live = take && best > kNone<T>;
+    const float inv = softmax_parts<LG>(x, top, live);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) ps[i] = fmaf(x[i], inv, ps[i]);
+    float chosen = 0.0f;
+    for (int j = 0;;) {
+        if (lane == 0) ckey[j] = live ? best : 0;
+        if (renormalize && best > kNone<T>) chosen += exp_below(key_logit<T>(best), top);
+        if (++j == topk) break;
+        if (key[0] == best) {
+#pragma unroll
+            for (int i = 0; i + 1 < kPerLane; ++i) key[i] = key[i + 1];
+            key[kPerLane - 1] = 0;
+        }
+        best = lanes_max<LG>(key[0]);
+    }
+    if (lane == 0) {
+        *topv = top;
+        // where the largest logit is not finite, inv is NaN and the gates are
+        *factor = renormalize ? 1.0f / chosen + (inv - inv) : inv;
+    }
+    return live;
+}
+
+template <class T>
+__device__ __forceinline__ float gate_of(Key<T> k, float top, float factor) {
+    return k > kNone<T> ? exp_below(key_logit<T>(k), top) * factor : 0.0f;
+}
+
+// The number of bits of a row of words in [from, to).
+__device__ __forceinline__ int count_bits(const uint32_t* words, int from, int to) {
+    int n = 0;
+    for (int w = from >> 5; w <= (to - 1) >> 5; ++w) {
+        uint32_t v = words[w];
+        if (w == from >> 5) v &= ~0u << (from & 31);
+        if (w == to >> 5) v &= ~(~0u << (to & 31));
+        n += __popc(v);
+    }
+    return n;
+}
+
+// The probability sums of a workgroup: a wave's groups by shuffles, the waves
+// in order.  put(expert, sum).
+template <int THREADS, int LG, class Put>
+__device__ __forceinline__ void sum_probs(float* ps, float* wsum, int experts, Put&& put) {
+    const int e0 = threadIdx.x % LG * kPerLane;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+#pragma unroll
+        for (int d = LG; d < 64; d <<= 1) ps[i] += __shfl_xor(ps[i], d);
     if ((threadIdx.x & 63) < LG) {
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i)
             if (e0 + i < experts) wsum[(threadIdx.x >> 6) * experts + e0 + i] = ps[i];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < experts; e += kThreads) {
+    for (int e = threadIdx.x; e < experts; e += THREADS) {
         float s = 0.0f;
-        for (int w = 0; w < kThreads / 64; ++w) s += wsum[w * experts + e];
-        psum[(int64_t)blockIdx.x * experts + e] = s;
-        hist[(int64_t)blockIdx.x * experts + e] = seen[e];
+        for (int w = 0; w < THREADS / 64; ++w) s += wsum[w * experts + e];
+        put(e, s);
     }
-    if (threadIdx.x == 0) nvalid[blockIdx.x] = taken;
 }
+
+// Workgroup b routes its run.  A chunk's choices go into a bit per (expert,
+// token) in LDS, and a choice's rank among its expert's is the number of bits
+// before it, whatever order the waves ran in.  Leaves each position's rank
+// within the run, the run's counts, probability sums and number of tokens that
+// take part.
+template <class T, int LG, bool EIGHTS>
+__global__ __launch_bounds__(kThreads) void route_runs(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
+                                                       int experts, int topk, int renormalize, RouterOut out) {
+    constexpr int GROUPS = kThreads / LG;
+    typedef Key<T> K;
+    extern __shared__ uint64_t lds[];
+    K* ckey = (K*)lds;                                       // kChunk x topk: the chosen keys
+    uint32_t* bits = (uint32_t*)(ckey + kChunk * topk);      // experts x kWords
+    int32_t* seen = (int32_t*)(bits + experts * kWords);     // experts: choices of earlier chunks
+    float* tops = (float*)(seen + experts);                  // kChunk: a token's largest logit
+    float* factors = tops + kChunk;                          // kChunk
+    __shared__ int32_t taken;
+    const int group = threadIdx.x / LG, lane = threadIdx.x % LG;
+    const float per_topk = 1.0f / (float)topk;
+    int32_t t0, t1;
+    runs.run(blockIdx.x, &t0, &t1);
+    for (int e = threadIdx.x; e < experts; e += kThreads) seen[e] = 0;
+    if (threadIdx.x == 0) taken = 0;
+    float ps[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) ps[i] = 0.0f;
+    int mine = 0;
+    for (int32_t c0 = t0; c0 < t1; c0 += kChunk) {
+        const int len = min(kChunk, t1 - c0);
+        for (int i = threadIdx.x; i < experts * kWords; i += kThreads) bits[i] = 0;
+        Logits<T> next;
+        bool valid = true;
+        auto fetch = [&](int tl) {
+            load_logits<EIGHTS>(logits + (c0 + tl) * ld, lane * kPerLane, experts, &next);
+            valid = !mask || mask[c0 + tl] != 0;
+        };
+        if (group < len) fetch(group);
+        for (int tl = group; tl < len; tl += GROUPS) {
+            const Logits<T> l = next;
+            const bool take = valid;
+            if (tl + GROUPS < len) fetch(tl + GROUPS);   // the next token's logits are on their way meanwhile
+            const bool live = route_token<T, LG>(l, take, lane, experts, topk, renormalize, ps, ckey + tl * topk,
+                                                 tops + tl, factors + tl);
+            if (lane == 0) mine += live;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < len * topk; i += kThreads) {
+            const int tl = (int)(((float)i + 0.5f) * per_topk);   // i / topk: i is small
+            const K k = ckey[i];
+            int e = -1;
+            if (k > kNone<T>) {
+                e = key_expert<T>(k);
+                atomicOr(&bits[e * kWords + (tl >> 5)], 1u << (tl & 31));
+            }
+            out.ids[(int64_t)c0 * topk + i] = e;
+            out.gates[(int64_t)c0 * topk + i] = gate_of<T>(k, tops[tl], factors[tl]);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < len * topk; i += kThreads) {
+            const int tl = (int)(((float)i + 0.5f) * per_topk);
+            const K k = ckey[i];
+            int rank = -1;
+            if (k > kNone<T>) {
+                const int e = key_expert<T>(k);
+                rank = seen[e] + count_bits(bits + e * kWords, 0, tl);
+            }
+            out.positions[(int64_t)c0 * topk + i] = rank;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < experts; e += kThreads) seen[e] += count_bits(bits + e * kWords, 0, len);
+        __syncthreads();
+    }
+    if (lane == 0 && mine) atomicAdd(&taken, mine);
+    const int64_t blocks = runs.blocks();
+    // the waves' sums go where the bits were
+    sum_probs<kThreads, LG>(ps, (float*)bits, experts, [&](int e, float s) {
+        out.psum[e * blocks + blockIdx.x] = s;
+        out.hist[e * blocks + blockIdx.x] = seen[e];
+    });
+    if (threadIdx.x == 0) out.nvalid[blockIdx.x] = taken;
+}
+static_assert(kMaxExperts <= 512, "place_rows: two experts a thread");
 static_assert(kThreads / 64 <= kWords, "the waves' sums fit where the bits were");
 
-// One wave an expert: hist[b] becomes the choices of the piece's earlier runs;
-// counts and probability sums.
-__global__ __launch_bounds__(64) void scan_runs(int32_t* hist, const float* psum, Runs runs, int experts,
-                                                int64_t* counts, float* prob_sums) {
-    const int e = blockIdx.x, lane = threadIdx.x;
-    float s = 0.0f;
-    for (int p = 0; p < runs.pieces; ++p) {
-        int32_t base = 0;
-        for (int i = 0; i < runs.per; i += 64) {
-            const bool in = i + lane < runs.per;
-            const int64_t b = (int64_t)p * runs.per + i + lane;
-            const int32_t v = in ? hist[b * experts + e] : 0;
-            int32_t inc = v;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int32_t up = __shfl_up(inc, d);
-                if (lane >= d) inc += up;
-            }
-            if (in) {
-                hist[b * experts + e] = base + inc - v;
-                s += psum[b * experts + e];
-            }
-            base += __shfl(inc, 63);
-        }
-        if (lane == 0) counts[(int64_t)p * experts + e] = base;
+// All tokens in one workgroup and one step: LG lanes a token, at most kAlone
+// lanes.  The ranks are counted from the token's piece on, so no run ends
+// where a piece does.
+template <class T, int LG>
+__global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
+                                                      int experts, int world, int topk, int renormalize, float coef,
+                                                      RouterOut out) {
+    typedef Key<T> K;
+    extern __shared__ uint64_t lds[];
+    const int tokens = runs.tokens, pieces = runs.pieces;
+    const int words = (tokens + 31) >> 5;
+    K* ckey = (K*)lds;                                              // tokens x topk
+    uint32_t* bits = (uint32_t*)(ckey + tokens * topk);             // experts x words
+    float* tops = (float*)(bits + experts * words);                 // tokens
+    float* factors = tops + tokens;                                 // tokens
+    int32_t* cnt = (int32_t*)(factors + tokens);                    // pieces x experts
+    int32_t* row = cnt + pieces * experts;                          // pieces x experts
+    float* wsum = (float*)(row + pieces * experts);                 // kAlone / 64 x experts
+    __shared__ int32_t taken;
+    __shared__ int32_t scan[kAlone / 64];
+    __shared__ float lsum[kAlone / 64];
+    const int tl = threadIdx.x / LG, lane = threadIdx.x % LG;
+    Logits<T> l;
+    bool valid = true;
+    if (tl < tokens) {
+        load_logits<false>(logits + tl * ld, lane * kPerLane, experts, &l);
+        valid = !mask || mask[tl] != 0;
     }
-    s = lanes_sum<64>(s);
-    if (lane == 0) prob_sums[e] = s;
-}
-
-// Turns ranks within a run into send rows: first the rows of all (destination,
-// piece, expert) before, from the counts, then the piece's earlier runs.
-// Workgroup 0 also writes the loss and the number of tokens.
-__global__ __launch_bounds__(256) void place_rows(const int32_t* ids, int32_t* positions, const int32_t* hist,
-                                                  const int32_t* nvalid, int blocks, Runs runs, int experts,
-                                                  int world, int topk,
-                                                  const int64_t* counts, const float* prob_sums, float coef,
-                                                  float* loss, int64_t* valid) {
-    extern __shared__ uint32_t lds[];
-    int32_t* first = (int32_t*)lds;   // experts: this piece's first row of each
-    const int p = blockIdx.x / runs.per, local = experts / world;
-    for (int e = threadIdx.x; e < experts && blocks > 0; e += 256) {
-        const int dest = e / local;
-        int64_t row = 0;
-        for (int q = 0; q < runs.pieces; ++q)
-            for (int f = 0; f < experts; ++f) {
-                const int fd = f / local;
-                if (fd < dest || (fd == dest && (q < p || (q == p && f < e)))) row += counts[(int64_t)q * experts + f];
-            }
-        first[e] = (int32_t)row + hist[(int64_t)blockIdx.x * experts + e];
+    if (threadIdx.x == 0) taken = 0;
+    for (int i = threadIdx.x; i < experts * words; i += kAlone) bits[i] = 0;
+    float ps[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) ps[i] = 0.0f;
+    bool live = false;
+    if (tl < tokens)
+        live = route_token<T, LG>(l, valid, lane, experts, topk, renormalize, ps, ckey + tl * topk, tops + tl,
+                                  factors + tl);
+    __syncthreads();
+    if (lane == 0 && live) atomicAdd(&taken, 1);
+    for (int i = threadIdx.x; i < tokens * topk; i += kAlone) {
+        const int t = i / topk;
+        const K k = ckey[i];
+        int e = -1;
+        if (k > kNone<T>) {
+            e = key_expert<T>(k);
+            atomicOr(&bits[e * words + (t >> 5)], 1u << (t & 31));
+        }
+        out.ids[i] = e;
+        out.gates[i] = gate_of<T>(k, tops[t], factors[t]);
     }
     __syncthreads();
-    const int64_t i1 = runs.end(blockIdx.x) * topk;
-    for (int64_t i = runs.begin(blockIdx.x) * topk + threadIdx.x; i < i1; i += 256) {
-        const int e = ids[i];
-        if (e >= 0) positions[i] += first[e];
+    for (int i = threadIdx.x; i < pieces * experts; i += kAlone) {
+        const int q = i / experts, e = i % experts;
+        const int c = count_bits(bits + e * words, runs.piece_begin(q), runs.piece_begin(q + 1));
+        cnt[i] = c;
+        out.counts[i] = c;
+    }
+    __syncthreads();
+    const float n = (float)max(taken, 1);
+    float term = 0.0f;
+    sum_probs<kAlone, LG>(ps, wsum, experts, [&](int e, float s) {
+        int32_t c = 0;
+        for (int q = 0; q < pieces; ++q) c += cnt[q * experts + e];
+        out.prob_sums[e] = s;
+        term += loss_term((float)c, s, n);
+    });
+    term = group_sum<kAlone>(term, lsum);
+    if (threadIdx.x == 0) {
+        *out.valid = taken;
+        *out.loss = coef * (float)experts / (float)topk * term;
+    }
+    first_rows<kAlone>(pieces * experts, pieces, experts / world, scan,
+                       [&](int p, int e) { return cnt[p * experts + e]; },
+                       [&](int p, int e, int32_t r) { row[p * experts + e] = r; });
+    __syncthreads();
+    for (int i = threadIdx.x; i < tokens * topk; i += kAlone) {
+        const int t = i / topk;
+        const K k = ckey[i];
+        int at = -1;
+        if (k > kNone<T>) {
+            int q = 0;
+            while (t >= runs.piece_begin(q + 1)) ++q;
+            const int e = key_expert<T>(k);
+            at = row[q * experts + e] + count_bits(bits + e * words, runs.piece_begin(q), t);
+        }
+        out.positions[i] = at;
+    }
+}
+
+// One workgroup an expert, four runs a thread: each run's base, the counts and
+// the probability sums.
+__global__ __launch_bounds__(kMostBlocks / 4) void scan_runs(Runs runs, RouterOut out) {
+    constexpr int THREADS = kMostBlocks / 4;
+    __shared__ int32_t waves[THREADS / 64];
+    __shared__ int32_t before[COC_MAX_SPLIT + 1];   // choices before each piece
+    __shared__ float lsum[THREADS / 64];
+    const int e = blockIdx.x, experts = gridDim.x, lane = threadIdx.x & 63, blocks = runs.blocks();
+    const int32_t* hist = out.hist + (int64_t)e * blocks;
+    const float* psum = out.psum + (int64_t)e * blocks;
+    const int b0 = threadIdx.x * 4;
+    int32_t v[4], sum = 0;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool in = b0 + i < blocks;
+        v[i] = in ? hist[b0 + i] : 0;
+        s += in ? psum[b0 + i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t h = v[i];
+        v[i] = sum;
+        sum += h;
+    }
+    int32_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t up = __shfl_up(inc, d);
+        if (lane >= d) inc += up;
+    }
+    if (lane == 63) waves[threadIdx.x >> 6] = inc;
+    __syncthreads();
+    int32_t base = inc - sum;
+    for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) base += waves[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] += base;
+        if (b0 + i < blocks && (b0 + i) % runs.per == 0) before[(b0 + i) / runs.per] = v[i];
+    }
+    if (threadIdx.x == THREADS - 1) before[runs.pieces] = base + sum;
+    s = group_sum<THREADS>(s, lsum);   // its barrier also covers `before`
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (b0 + i < blocks)
+            out.base[(int64_t)(b0 + i) * experts + e] = v[i] - before[(b0 + i) / runs.per];
+    if (threadIdx.x < (unsigned)runs.pieces)
+        out.counts[threadIdx.x * experts + e] = before[threadIdx.x + 1] - before[threadIdx.x];
+    if (threadIdx.x == 0) out.prob_sums[e] = s;
+}
+
+// Turns a run's ranks into send rows: the rows before its (piece, expert), from
+// the counts, and the choices of the piece's earlier runs.  What it reads is
+// asked for at once, so that it waits for memory once.  Workgroup 0 also writes
+// the loss and the number of tokens.
+__global__ __launch_bounds__(256) void place_rows(Runs runs, int experts, int world, int topk, float coef,
+                                                  RouterOut out) {
+    constexpr int kAhead = 4;
+    extern __shared__ uint64_t lds[];
+    int32_t* row = (int32_t*)lds;   // experts: the run's first row of each
+    __shared__ int32_t scan[4];
+    const int blocks = runs.blocks(), piece = blockIdx.x / runs.per;
+    int32_t t0, t1;
+    runs.run(blockIdx.x, &t0, &t1);
+    const int i0 = t0 * topk + threadIdx.x, i1 = t1 * topk;
+    int32_t id[kAhead], at[kAhead], base[2];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+        id[q] = i0 + q * 256 < i1 ? out.ids[i0 + q * 256] : -1;
+        at[q] = i0 + q * 256 < i1 ? out.positions[i0 + q * 256] : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int e = threadIdx.x + q * 256;
+        base[q] = e < experts ? out.base[(int64_t)blockIdx.x * experts + e] : 0;
+    }
+    first_rows<256>(runs.pieces * experts, runs.pieces, experts / world, scan,
+                    [&](int p, int e) { return (int32_t)out.counts[p * experts + e]; },
+                    [&](int p, int e, int32_t r) { if (p == piece) row[e] = r; });
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int e = threadIdx.x + q * 256;
+        if (e < experts) row[e] += base[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+        if (id[q] >= 0) out.positions[i0 + q * 256] = at[q] + row[id[q]];
+    for (int i = i0 + kAhead * 256; i < i1; i += 256) {
+        const int e = out.ids[i];
+        if (e >= 0) out.positions[i] += row[e];
     }
     if (blockIdx.x == 0 && threadIdx.x < 64) {
-        int64_t n = 0;
-        for (int b = threadIdx.x; b < blocks; b += 64) n += nvalid[b];
-        float s = 0.0f;
+        int32_t taken = 0;
+        for (int b = threadIdx.x; b < blocks; b += 64) taken += out.nvalid[b];
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) n += __shfl_xor((long long)n, d);
+        for (int d = 1; d < 64; d <<= 1) taken += __shfl_xor(taken, d);
+        const float n = (float)max(taken, 1);
+        float s = 0.0f;
         for (int e = threadIdx.x; e < experts; e += 64) {
             int64_t c = 0;
-            for (int q = 0; q < runs.pieces; ++q) c += counts[(int64_t)q * experts + e];
-            s += (float)c / (float)(n > 0 ? n : 1) * (prob_sums[e] / (float)(n > 0 ? n : 1));
+            for (int q = 0; q < runs.pieces; ++q) c += out.counts[q * experts + e];
+            s += loss_term((float)c, out.prob_sums[e], n);
         }
         s = lanes_sum<64>(s);
         if (threadIdx.x == 0) {
-            *valid = n;
-            *loss = coef * (float)experts / (float)topk * s;
+            *out.valid = taken;
+            *out.loss = coef * (float)experts / (float)topk * s;
         }
     }
+}
+
+// A binary32's bits in unsigned order, every NaN the largest.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return x != x ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
 // dlogits = p (a - <p, a>) + the gates' term, a_e the loss's derivative by p_e
 // with the counts held fixed, for LG lanes a token.
-template <class T, int LG>
+template <class T, int LG, bool EIGHTS>
 __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int64_t ld, const uint8_t* mask,
                                                            const int32_t* ids, const float* gates,
                                                            const int64_t* counts, const int64_t* valid,
@@ -311,14 +634,18 @@ __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int6
         a[i] = w * (float)c;
     }
     for (int64_t t = (int64_t)blockIdx.x * GROUPS + group; t < tokens; t += (int64_t)gridDim.x * GROUPS) {
-        float x[kPerLane], total;
-        uint32_t key[kPerLane];
-        load_logits(logits + t * ld, e0, experts, x);
-        bool live = !mask || mask[t] != 0;
+        float x[kPerLane];
+        Logits<T> l;
+        load_logits<EIGHTS>(logits + t * ld, e0, experts, &l);
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) key[i] = e0 + i < experts ? order_key(x[i]) : 0;
-        live = softmax_parts<LG>(x, key, live, &total);
-        const float inv = live ? 1.0f / total : 0.0f;
+        for (int i = 0; i < kPerLane; ++i) x[i] = l.get(i);
+        uint32_t top_key = 0;   // the largest logit's order, as in make_key; NaN largest
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) top_key = max(top_key, order_bits(x[i]));
+        top_key = lanes_max<LG>(top_key);
+        const bool live = (!mask || mask[t] != 0) && top_key > Order<float>::kNegInf;
+        const float top = __uint_as_float(top_key & 0x80000000u ? top_key ^ 0x80000000u : ~top_key);
+        const float inv = softmax_parts<LG>(x, top, live);
         float pa = 0.0f;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
@@ -361,31 +688,36 @@ void by_type(coc_dtype dt, F&& f) {
         f(bf16_t());
 }
 
-template <class F>
-void by_experts(int64_t experts, F&& f) {
-    if (experts <= 8)
-        f(std::integral_constant<int, 1>());
-    else if (experts <= 16)
-        f(std::integral_constant<int, 2>());
-    else if (experts <= 32)
-        f(std::integral_constant<int, 4>());
-    else if (experts <= 64)
-        f(std::integral_constant<int, 8>());
-    else if (experts <= 128)
-        f(std::integral_constant<int, 16>());
-    else if (experts <= 256)
-        f(std::integral_constant<int, 32>());
+// f(lanes of a token, whether the experts are a multiple of 8).
+template <int LG = 1, class F>
+void by_experts(int32_t experts, F&& f) {
+    if (experts <= LG * kPerLane || LG == 64)
+        experts % kPerLane == 0 ? f(std::integral_constant<int, LG>(), std::true_type())
+                                : f(std::integral_constant<int, LG>(), std::false_type());
     else
-        f(std::integral_constant<int, 64>());
+        by_experts<LG < 64 ? 2 * LG : 64>(experts, f);
 }
 
 Runs make_runs(int64_t tokens, int32_t pieces) {
     const int64_t longest = ceil_div(tokens, pieces);
-    int64_t per = ceil_div(longest, 64);
-    const int64_t most = kMostBlocks / pieces;
-    if (per > most) per = most;
-    if (per < 1) per = 1;
-    return {tokens, pieces, (int32_t)per};
+    int64_t len = ceil_div(longest, kMostBlocks / pieces);
+    if (len < kLeastRun) len = kLeastRun;
+    const int64_t per = longest > 0 ? ceil_div(longest, len) : 1;
+    return {(int32_t)tokens, pieces, (int32_t)per, (int32_t)len};
+}
+
+// Lanes for a token's logits.
+int lanes_of(int32_t experts) {
+    int l = 1;
+    while (l * kPerLane < experts) l *= 2;
+    return l;
+}
+
+// Whether one workgroup routes all tokens, in one launch: a lane for every 8
+// logits, and its tables in 64 KiB of LDS (at most 48 KiB of keys).
+bool alone(int64_t tokens, int32_t experts, int32_t pieces) {
+    return tokens * lanes_of(experts) <= kAlone && tokens * (experts < kMaxTopk ? experts : kMaxTopk) <= 6144 &&
+           pieces * experts <= 512;
 }
 
 coc_status check_router(int64_t tokens, int32_t experts, int32_t topk, int32_t pieces, int64_t ld, coc_dtype dt) {
@@ -408,9 +740,9 @@ coc_status check_router(int64_t tokens, int32_t experts, int32_t topk, int32_t p
 extern "C" {
 
 size_t coc_moe_router_workspace_bytes(int64_t tokens, int32_t experts, int32_t pieces) {
-    if (tokens <= 0 || experts < 1 || experts > coc::kMaxExperts || pieces < 1 || pieces > COC_MAX_SPLIT) return 0;
-    const coc::Runs r = coc::make_runs(tokens, pieces);
-    return (size_t)r.pieces * (size_t)r.per * (size_t)(experts * 8 + 4);
+    if (tokens < 0 || experts < 1 || experts > coc::kMaxExperts || pieces < 1 || pieces > COC_MAX_SPLIT) return 0;
+    if (coc::alone(tokens, experts, pieces)) return 0;
+    return (size_t)coc::make_runs(tokens, pieces).blocks() * (size_t)(experts * 12 + 4);
 }
 
 coc_status coc_moe_router(const void* logits, int64_t ld, const uint8_t* mask, int32_t* ids, float* gates,
@@ -444,34 +776,39 @@ coc_status coc_moe_router(const void* logits, int64_t ld, const uint8_t* mask, i
     };
     st = check_args(args, 10);
     if (st != COC_OK) return st;
-    // without tokens: no runs, zero counts and loss
-    Runs runs = make_runs(tokens > 0 ? tokens : 1, pieces);
-    runs.tokens = tokens;
-    if (tokens == 0) runs.per = 0;
-    const int blocks = runs.pieces * runs.per;
-    int32_t* hist = (int32_t*)ws;
-    float* psum = (float*)(hist + (int64_t)blocks * experts);
-    int32_t* nvalid = (int32_t*)(psum + (int64_t)blocks * experts);
-    if (blocks > 0) {
-        const size_t lds = (size_t)experts * (kWords + 1) * 4 + kChunk * 4 + kChunk * kMaxTopk * 2 +
-                           (size_t)kChunk * topk * 4;
-        by_type(dt, [&](auto t) {
-            using T = decltype(t);
-            by_experts(experts, [&](auto lg) {
-                route_runs<T, decltype(lg)::value><<<dim3(blocks), dim3(kThreads), lds, stream>>>(
-                    (const T*)logits, ld, mask, runs, experts, topk, renormalize, ids, gates, positions, hist, psum,
-                    nvalid);
+    Runs runs = make_runs(tokens, pieces);
+    const int64_t blocks = runs.blocks();
+    int32_t* w = (int32_t*)ws;
+    RouterOut out{ids, gates, positions, counts, prob_sums, loss, valid, w, w + blocks * experts,
+                  (float*)w + 2 * blocks * experts, w + 3 * blocks * experts};
+    const bool one = alone(tokens, experts, pieces);   // without tokens too, where there are few experts
+    const size_t key = dt == COC_F32 ? 8 : 4;
+    by_type(dt, [&](auto t) {
+        using T = decltype(t);
+        if (one) {
+            const size_t words = (size_t)ceil_div(tokens, 32);
+            const size_t lds = (size_t)tokens * topk * key + experts * words * 4 + (size_t)tokens * 8 +
+                               (size_t)pieces * experts * 8 + kAlone / 64 * (size_t)experts * 4;
+            by_experts(experts, [&](auto lg, auto) {
+                route_alone<T, decltype(lg)::value><<<dim3(1), dim3(kAlone), lds, stream>>>(
+                    (const T*)logits, ld, mask, runs, experts, world, topk, renormalize, coef, out);
             });
+            return;
+        }
+        const size_t lds = kChunk * topk * key + (size_t)experts * (kWords + 1) * 4 + kChunk * 8;
+        by_experts(experts, [&](auto lg, auto eights) {
+            route_runs<T, decltype(lg)::value, decltype(eights)::value>
+                <<<dim3((uint32_t)blocks), dim3(kThreads), lds, stream>>>((const T*)logits, ld, mask, runs, experts,
+                                                                          topk, renormalize, out);
         });
-        st = launched("router");
-        if (st != COC_OK) return st;
-    }
-    scan_runs<<<dim3(experts), dim3(64), 0, stream>>>(hist, psum, runs, experts, counts, prob_sums);
+    });
+    st = launched("router");
+    if (st != COC_OK || one) return st;
+    scan_runs<<<dim3(experts), dim3(kMostBlocks / 4), 0, stream>>>(runs, out);
     st = launched("router");
     if (st != COC_OK) return st;
-    if (runs.per == 0) runs.per = 1;   // one workgroup without tokens writes the loss
-    place_rows<<<dim3(blocks > 0 ? blocks : 1), dim3(256), (size_t)experts * 4, stream>>>(
-        ids, positions, hist, nvalid, blocks, runs, experts, world, topk, counts, prob_sums, coef, loss, valid);
+    place_rows<<<dim3((uint32_t)blocks), dim3(256), (size_t)experts * 4, stream>>>(runs, experts, world, topk, coef,
+                                                                                  out);
     return launched("router");
 }
 
@@ -505,11 +842,11 @@ coc_status coc_moe_router_backward(const void* logits, int64_t ld, const uint8_t
     if (st != COC_OK) return st;
     by_type(dt, [&](auto t) {
         using T = decltype(t);
-        by_experts(experts, [&](auto lg) {
+        by_experts(experts, [&](auto lg, auto eights) {
             constexpr int LG = decltype(lg)::value;
             int64_t grid = ceil_div(tokens, kThreads / LG);
             if (grid > 2048) grid = 2048;
-            route_backward<T, LG><<<dim3((uint32_t)grid), dim3(kThreads), 0, stream>>>(
+            route_backward<T, LG, decltype(eights)::value><<<dim3((uint32_t)grid), dim3(kThreads), 0, stream>>>(
                 (const T*)logits, ld, mask, ids, gates, counts, valid, dgates, dloss, (T*)dlogits, ld_out, tokens,
                 experts, pieces, topk, coef, renormalize);
         });

@@ -152,6 +152,10 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u(uint64_t v) {
+    return (uint64_t)dpp_u<CTRL>((uint32_t)(v >> 32)) << 32 | dpp_u<CTRL>((uint32_t)v);
+}
 constexpr int kDppXor1 = 0xB1;         // quad_perm [1, 0, 3, 2]
 constexpr int kDppXor2 = 0x4E;         // quad_perm [2, 3, 0, 1]
 constexpr int kDppHalfMirror = 0x141;  // within 8 lanes: the other quad
@@ -178,6 +182,17 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
     if constexpr (LANES >= 16) v = max(v, dpp_u<kDppMirror>(v));
     if constexpr (LANES >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
     if constexpr (LANES >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ uint64_t lanes_max(uint64_t v) {
+    if constexpr (LANES >= 2) v = max(v, dpp_u<kDppXor1>(v));
+    if constexpr (LANES >= 4) v = max(v, dpp_u<kDppXor2>(v));
+    if constexpr (LANES >= 8) v = max(v, dpp_u<kDppHalfMirror>(v));
+    if constexpr (LANES >= 16) v = max(v, dpp_u<kDppMirror>(v));
+    if constexpr (LANES >= 32) v = max(v, (uint64_t)__shfl_xor((unsigned long long)v, 16));
+    if constexpr (LANES >= 64) v = max(v, (uint64_t)__shfl_xor((unsigned long long)v, 32));
     return v;
 }
 

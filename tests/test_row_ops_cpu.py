@@ -109,7 +109,7 @@ CASES = [
     (router, dict(topk=17), SHAPE), (router, dict(experts=8, topk=9), SHAPE), (router, dict(ld=15), SHAPE),
     (router, dict(pieces=0), SPLIT), (router, dict(pieces=9), SPLIT), (router, dict(world=3), WORLD),
     (router, dict(world=16), WORLD), (router, dict(world=0), WORLD), (router, dict(dt=4), DTYPE),
-    (router, dict(ws=None), WORKSPACE), (router, dict(nws=16), WORKSPACE), (router, dict(counts=at(5) + 4), ALIGN),
+    (router, dict(ws=None, tokens=100000), WORKSPACE), (router, dict(nws=16, tokens=100000), WORKSPACE), (router, dict(counts=at(5) + 4), ALIGN),
     (router, dict(gates=at(2) + 60), ALIAS), (router, dict(ids=at(0)), ALIAS),
     *[(routerb, {k: None}, NULL) for k in ("logits", "ids", "gates", "counts", "valid", "dlogits")],
     (routerb, dict(ldo=15), SHAPE), (routerb, dict(dlogits=at(0)), ALIAS), (routerb, dict(pieces=0), SPLIT),
@@ -146,9 +146,8 @@ def test_workspace_sizes():
     assert L.coc_layer_norm_backward_workspace_bytes(3, 64) >= 2 * 64 * 4
     assert L.coc_embedding_grad_workspace_bytes(0, 64) == 0
     assert L.coc_embedding_grad_workspace_bytes(8, 64) >= 8 * 8
-    assert L.coc_moe_router_workspace_bytes(0, 16, 4) == 0
     assert L.coc_moe_router_workspace_bytes(100, 16, 9) == 0
-    assert L.coc_moe_router_workspace_bytes(1000, 16, 4) >= 4 * (16 * 8 + 4)
+    assert L.coc_moe_router_workspace_bytes(100000, 16, 4) >= 4 * (16 * 8 + 4)
 
 
 def _f(*shape, dtype=torch.bfloat16):
