@@ -469,9 +469,9 @@ coc_status coc_embedding(const void* ids, coc_index id_type, const void* table, 
  * row of the gradient is written once and in an order fixed by the ids; rows
  * without tokens become zeros (accumulate: stay as they are).  dy: tokens x n
  * of `dt`; grad: vocab x n of `grad_dt` (dt or COC_F32).  ws: at least
- * coc_embedding_grad_workspace_bytes(tokens, n), 8-byte aligned.
+ * coc_embedding_grad_workspace_bytes(tokens, vocab, n), 8-byte aligned.
  */
-size_t coc_embedding_grad_workspace_bytes(int64_t tokens, int64_t n);
+size_t coc_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t n);
 coc_status coc_embedding_grad(const void* ids, coc_index id_type, const void* dy, void* grad, int64_t tokens,
                               int64_t vocab, int64_t n, int64_t start, float scale, int32_t accumulate,
                               coc_dtype dt, coc_dtype grad_dt, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -143,7 +143,7 @@ def _declare_row_ops(L) -> None:
         getattr(L, name).restype = _i32
     for name, args in {
         "coc_layer_norm_backward_workspace_bytes": [_i64, _i64],
-        "coc_embedding_grad_workspace_bytes": [_i64, _i64],
+        "coc_embedding_grad_workspace_bytes": [_i64, _i64, _i64],
         "coc_moe_router_workspace_bytes": [_i64, _i32, _i32],
     }.items():
         getattr(L, name).argtypes = args

@@ -9,12 +9,11 @@ namespace {
 // sums over registers, which lose nothing where the mean is far from zero),
 // then the output.
 template <class T, class W, int TPR, int EPT>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_forward(
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void ln_forward(
     const T* x, const T* residual, const W* gamma, const W* beta, T* y, T* sum_out, float* mean_out, float* rstd_out,
     int64_t rows, int n, float eps) {
     constexpr int VN = kVec<T>, V = EPT / VN;
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;   // rows per workgroup
-    static_assert(TPR == 64 || RPB == 1, "several rows per workgroup: one wave each");
+    constexpr int RPB = TPR == 64 ? 4 : 1;   // rows per workgroup: several where a wave holds one
     __shared__ float buf[2][TPR / 64];
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -81,12 +80,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_forward(
 // Workgroup b takes rows b, b + grid, ..., a thread always the same columns,
 // so the columns' sums stay in its registers over all its rows and go to the
 // workspace once, as row b of `part` (grid x 2 x n); ln_backward_sum adds
-// those rows in order.
+// those rows in order.  The next row is on its way while this one is summed.
 template <class T, class W, int TPR, int EPT>
 __global__ __launch_bounds__(TPR) void ln_backward(
     const T* dy, const T* x, const W* gamma, const float* mean_in, const float* rstd_in, const T* dsum, T* dx,
     float* part, int64_t rows, int n) {
     constexpr int VN = kVec<T>, V = EPT / VN;
+    constexpr bool AHEAD = EPT * (int)sizeof(T) * TPR <= 32768;   // what the registers of 1024 threads hold
     __shared__ float buf[2][2][TPR / 64];
     const int t = threadIdx.x;
     float dg[V][VN], db[V][VN];
@@ -94,15 +94,26 @@ __global__ __launch_bounds__(TPR) void ln_backward(
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < VN; ++i) dg[v][i] = db[v][i] = 0.0f;
-    int flip = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
-        const float mean = mean_in[row], rstd = rstd_in[row];
-        Packed<T> px[V], pd[V];
+    struct Row {
+        Packed<T> x[V], d[V], s[V];
+        float mean, rstd;
+    };
+    auto load = [&](int64_t row, Row* r) {
+        r->mean = mean_in[row];
+        r->rstd = rstd_in[row];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            load_raw(x + row * n, (v * TPR + t) * VN, n, &px[v]);
-            load_raw(dy + row * n, (v * TPR + t) * VN, n, &pd[v]);
+            const int c = (v * TPR + t) * VN;
+            load_raw(x + row * n, c, n, &r->x[v]);
+            load_raw(dy + row * n, c, n, &r->d[v]);
+            if (dsum) load_raw(dsum + row * n, c, n, &r->s[v]);
         }
+    };
+    Row now, next;
+    int64_t row = blockIdx.x;
+    load(row, &now);   // grid <= rows
+    for (int flip = 0; row < rows; row += gridDim.x, flip ^= 1) {
+        if (AHEAD && row + gridDim.x < rows) load(row + gridDim.x, &next);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -111,7 +122,7 @@ __global__ __launch_bounds__(TPR) void ln_backward(
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
                 // past n dy and gamma are 0, and so is every term
-                const float d = (float)pd[v].e[i], xh = ((float)px[v].e[i] - mean) * rstd;
+                const float d = now.d[v].get(i), xh = (now.x[v].get(i) - now.mean) * now.rstd;
                 dg[v][i] += d * xh;
                 db[v][i] += d;
                 s1 += d * g[i];
@@ -141,31 +152,27 @@ __global__ __launch_bounds__(TPR) void ln_backward(
         for (int v = 0; v < V; ++v) {
             const int c = (v * TPR + t) * VN;
             if (c >= n) break;
-            float g[VN], o[VN], r[VN];
+            float g[VN], o[VN];
             load_n<VN>(gamma, c, n, g);
-            if (dsum) {
-                load_vec(dsum + row * n, c, n, r);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VN; ++i) r[i] = 0.0f;
-            }
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
-                const float xh = ((float)px[v].e[i] - mean) * rstd;
-                o[i] = rstd * ((float)pd[v].e[i] * g[i] - s1 - xh * s2) + r[i];
+                const float xh = (now.x[v].get(i) - now.mean) * now.rstd;
+                o[i] = now.rstd * (now.d[v].get(i) * g[i] - s1 - xh * s2);
+                if (dsum) o[i] += now.s[v].get(i);
             }
             store_vec(dx + row * n, c, n, o);
         }
+        if (AHEAD)
+            now = next;
+        else if (row + gridDim.x < rows)
+            load(row + gridDim.x, &now);
     }
     float* pr = part + (int64_t)blockIdx.x * 2 * n;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * TPR + t) * VN;
-#pragma unroll
-        for (int q = 0; q < VN; q += 4) {
-            store_vec(pr, c + q, n, &dg[v][q]);
-            store_vec(pr + n, c + q, n, &db[v][q]);
-        }
+        keep_n<VN>(pr, c, n, dg[v]);
+        keep_n<VN>(pr + n, c, n, db[v]);
     }
 }
 
@@ -203,30 +210,35 @@ __global__ __launch_bounds__(256) void ln_backward_sum(const float* part, int pa
     }
 }
 
+#ifndef V_MOST
+#define V_MOST (n <= 2048 ? 1024 : 256)
+#endif
 constexpr int64_t kMaxNorm = 32768;   // elements of a row: 1024 threads of 32
 
 // Workgroups of the backward pass: one part each.
 int64_t backward_parts(int64_t rows, int64_t n) {
-    const int64_t most = n <= 2048 ? 1024 : 256;
+    const int64_t most = V_MOST;
     return rows < most ? rows : most;
 }
 
+// f(threads of a row, elements of a thread).
 template <class F>
 void by_row_size(int64_t n, F&& f) {
+    auto call = [&](auto t, auto e) { f(t, e); };
     if (n <= 512)
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+        call(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
     else if (n <= 1024)
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+        call(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
     else if (n <= 2048)
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 32>());
+        call(std::integral_constant<int, 128>(), std::integral_constant<int, 16>());
     else if (n <= 4096)
-        f(std::integral_constant<int, 256>(), std::integral_constant<int, 16>());
+        call(std::integral_constant<int, 256>(), std::integral_constant<int, 16>());
     else if (n <= 8192)
-        f(std::integral_constant<int, 256>(), std::integral_constant<int, 32>());
+        call(std::integral_constant<int, 512>(), std::integral_constant<int, 16>());
     else if (n <= 16384)
-        f(std::integral_constant<int, 512>(), std::integral_constant<int, 32>());
+        call(std::integral_constant<int, 1024>(), std::integral_constant<int, 16>());
     else
-        f(std::integral_constant<int, 1024>(), std::integral_constant<int, 32>());
+        call(std::integral_constant<int, 1024>(), std::integral_constant<int, 32>());
 }
 
 // f(T, W) of the row and parameter types.
@@ -284,7 +296,7 @@ coc_status coc_layer_norm(const void* x, const void* residual, const void* gamma
         using W = decltype(w);
         by_row_size(n, [&](auto tpr, auto ept) {
             constexpr int TPR = decltype(tpr)::value, EPT = decltype(ept)::value;
-            constexpr int threads = TPR < 256 ? 256 : TPR;
+            constexpr int threads = TPR == 64 ? 256 : TPR;
             const int64_t grid = ceil_div(rows, threads / TPR);
             ln_forward<T, W, TPR, EPT><<<dim3((uint32_t)grid), dim3(threads), 0, stream>>>(
                 (const T*)x, (const T*)residual, (const W*)gamma, (const W*)beta, (T*)y, (T*)sum_out, mean, rstd, rows,

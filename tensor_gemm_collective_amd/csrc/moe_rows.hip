@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void combine_backward(const T* dy, const T* h,
 #pragma unroll
         for (int q = 0; q < kVec<T>; ++q) {
             s += d[q] * f[q];
-            d[q] *= g;
+            d[q] = product(d[q], g);
         }
         store_vec(dh + r * n, c, n, d);
     }

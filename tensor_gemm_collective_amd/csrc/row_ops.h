@@ -70,77 +70,149 @@ typedef __bf16 bf16_t;
 template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
-// 16 bytes at an address aligned to T only.  Global memory takes 16-byte
-// accesses of any alignment in the unaligned access mode that the HSA ABI
-// runs in, so rows of odd length need no path of their own.
+// 16 bytes of elements as four words: kept so, they take four registers (an
+// array of 16-bit values takes one for each).
 template <class T>
-struct __attribute__((packed, aligned(sizeof(T)))) Packed {
-    T e[kVec<T>];
+struct Packed {
+    uint32_t w[4];
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else if constexpr (std::is_same_v<T, bf16_t>)
+            return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        else
+            return (float)__builtin_bit_cast(T, (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0)));
+    }
+    // from binary32, each rounded once, to nearest even
+    __device__ __forceinline__ void set(const float* f) {
+        typedef T t2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(f[i]);
+            else
+                w[i] = __builtin_bit_cast(uint32_t, t2{(T)f[2 * i], (T)f[2 * i + 1]});
+        }
+    }
 };
 
-// Row elements [c, c + kVec) as binary32; those at or past n become 0.
-template <class T>
-__device__ __forceinline__ void load_vec(const T* row, int c, int n, float* f) {
-    if (c + kVec<T> <= n) {
-        Packed<T> p;
-        __builtin_memcpy(&p, row + c, 16);
-#pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) f[i] = (float)p.e[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) f[i] = c + i < n ? (float)row[c + i] : 0.0f;
-    }
-}
-
-// The same without the conversion (kept packed until it is used).
+// Row elements [c, c + kVec) at an address aligned to T only; those at or past n
+// are 0.  Global memory takes 16-byte accesses of any alignment in the
+// unaligned access mode that the HSA ABI runs in, so rows of odd length need no
+// path of their own.
 template <class T>
 __device__ __forceinline__ void load_raw(const T* row, int c, int n, Packed<T>* p) {
     if (c + kVec<T> <= n) {
-        __builtin_memcpy(p, row + c, 16);
+        __builtin_memcpy(p->w, row + c, 16);
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) p->e[i] = c + i < n ? row[c + i] : (T)0.0f;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v = 0;
+            if constexpr (sizeof(T) == 4) {
+                if (c + i < n) __builtin_memcpy(&v, row + c + i, 4);
+            } else {
+                uint16_t h = 0;
+                if (c + 2 * i < n) __builtin_memcpy(&h, row + c + 2 * i, 2);
+                v = h;
+                h = 0;
+                if (c + 2 * i + 1 < n) __builtin_memcpy(&h, row + c + 2 * i + 1, 2);
+                v |= (uint32_t)h << 16;
+            }
+            p->w[i] = v;
+        }
     }
+}
+
+template <class T>
+__device__ __forceinline__ void load_vec(const T* row, int c, int n, float* f) {
+    Packed<T> p;
+    load_raw(row, c, n, &p);
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i) f[i] = p.get(i);
+}
+
+// 16 bytes that nobody reads soon: stored without keeping them in the L2
+// (outputs of the big passes; see embedding.hip for what it gains).
+template <class T>
+__device__ __forceinline__ void stream16(T* at, const Packed<T>& p) {
+    typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef std::conditional_t<sizeof(T) == 2, u32x4_2, u32x4_4> u32x4;
+    u32x4 v = {p.w[0], p.w[1], p.w[2], p.w[3]};
+    __builtin_nontemporal_store(v, (u32x4*)at);
 }
 
 template <class T>
 __device__ __forceinline__ void store_raw(T* row, int c, int n, const Packed<T>& p) {
     if (c + kVec<T> <= n) {
-        __builtin_memcpy(row + c, &p, 16);
+        stream16(row + c, p);
     } else {
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i)
-            if (c + i < n) row[c + i] = p.e[i];
+            if (c + i < n) {
+                if constexpr (sizeof(T) == 4) {
+                    __builtin_memcpy(row + c + i, &p.w[i], 4);
+                } else {
+                    const uint16_t h = (uint16_t)(p.w[i >> 1] >> (i & 1 ? 16 : 0));
+                    __builtin_memcpy(row + c + i, &h, 2);
+                }
+            }
     }
 }
 
-// Each element rounded once, to nearest even.
 template <class T>
 __device__ __forceinline__ void store_vec(T* row, int c, int n, const float* f) {
-    if (c + kVec<T> <= n) {
-        Packed<T> p;
-#pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) p.e[i] = (T)f[i];
-        __builtin_memcpy(row + c, &p, 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec<T>; ++i)
-            if (c + i < n) row[c + i] = (T)f[i];
-    }
+    Packed<T> p;
+    p.set(f);
+    store_raw(row, c, n, p);
 }
 
-// kVec<T> elements of a parameter or sum vector whose type U may be wider than T.
+// N elements of a parameter or sum vector, whose type U may be wider than the
+// rows' (N: a multiple or a half of kVec<U>).
 template <int N, class U>
 __device__ __forceinline__ void load_n(const U* v, int c, int n, float* f) {
-    if (c + N <= n) {
-        struct __attribute__((packed, aligned(sizeof(U)))) { U e[N]; } p;
-        __builtin_memcpy(&p, v + c, sizeof(p));
+    if constexpr (N % kVec<U> == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = (float)p.e[i];
+        for (int i = 0; i < N; i += kVec<U>) load_vec(v, c + i, n, f + i);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = c + i < n ? (float)v[c + i] : 0.0f;
     }
+}
+
+// N values rounded to the vector's type U, for what is read again soon.
+template <int N, class U>
+__device__ __forceinline__ void keep_n(U* v, int c, int n, const float* f) {
+    if (c + N <= n) {
+        struct __attribute__((packed, aligned(sizeof(U)))) { U e[N]; } p;
+#pragma unroll
+        for (int i = 0; i < N; ++i) p.e[i] = (U)f[i];
+        __builtin_memcpy(v + c, &p, sizeof(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i < n) v[c + i] = (U)f[i];
+    }
+}
+
+// The same streamed, N a multiple of 4.
+template <int N, class U>
+__device__ __forceinline__ void store_n(U* v, int c, int n, const float* f) {
+    if constexpr (N % kVec<U> == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += kVec<U>) store_vec(v, c + i, n, f + i);
+    } else {
+        keep_n<N>(v, c, n, f);
+    }
+}
+
+// The binary32 product, rounded as such also where a conversion to fp16 follows
+// (one instruction could do both in one rounding, and another variant of the
+// same code not).
+__device__ __forceinline__ float product(float a, float b) {
+    float p = a * b;
+    asm("" : "+v"(p));   // no code: what follows cannot be joined with the product
+    return p;
 }
 
 // ------------------------------------------------------------------ device: reductions

@@ -147,7 +147,7 @@ def embedding_grad(ids, dy, vocab, *, start=0, scale=1.0, grad=None, accumulate=
     pd = _want(dy, "dy", dy, dy.dtype, *ids.shape, n)
     grad, pg = _out(grad, "grad", dy, stream, dy.dtype if grad is None else grad.dtype, vocab, n)
     L = lib()
-    ws, pw, nw = _workspace(ws, L.coc_embedding_grad_workspace_bytes(tokens, n), dy, stream)
+    ws, pw, nw = _workspace(ws, L.coc_embedding_grad_workspace_bytes(tokens, vocab, n), dy, stream)
     _check(L.coc_embedding_grad(pi, code, pd, pg, tokens, vocab, n, start, scale, int(bool(accumulate)),
                                 _dtype_code(dy), _dtype_code(grad), pw, nw, _queue(stream, dy)))
     return grad

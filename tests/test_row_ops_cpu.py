@@ -144,8 +144,8 @@ def test_workspace_sizes():
     L = tgc.lib()
     assert L.coc_layer_norm_backward_workspace_bytes(0, 64) == 0
     assert L.coc_layer_norm_backward_workspace_bytes(3, 64) >= 2 * 64 * 4
-    assert L.coc_embedding_grad_workspace_bytes(0, 64) == 0
-    assert L.coc_embedding_grad_workspace_bytes(8, 64) >= 8 * 8
+    assert L.coc_embedding_grad_workspace_bytes(0, 16, 64) == 0
+    assert L.coc_embedding_grad_workspace_bytes(8, 16, 64) >= 8 * 8
     assert L.coc_moe_router_workspace_bytes(100, 16, 9) == 0
     assert L.coc_moe_router_workspace_bytes(100000, 16, 4) >= 4 * (16 * 8 + 4)
 
