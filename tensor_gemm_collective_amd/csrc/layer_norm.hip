@@ -4,11 +4,32 @@
 namespace coc {
 namespace {
 
+// The parameters beside a vector of a row, kept as stored.
+template <class T, class W, RowKind KIND>
+struct Params {
+    static constexpr int V = (kVec<T> + kVec<W> - 1) / kVec<W>;
+    Packed<W> p[V];
+    __device__ __forceinline__ void load(const W* v, const Cols<T, KIND>& col, int n) {
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            if constexpr (KIND == kTiny)
+                load_raw(v, col.c + q * kVec<W>, n, &p[q]);
+            else
+                __builtin_memcpy(p[q].w, v + col.c + q * kVec<W>, 16);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return p[i / kVec<W>].get(i % kVec<W>); }
+    __device__ __forceinline__ void again() {
+#pragma unroll
+        for (int q = 0; q < V; ++q) repack(p[q]);
+    }
+};
+
 // Forward.  TPR threads hold one row in registers, EPT elements each, so a row
 // is read once: its mean, then the mean of its squared distances from it (two
 // sums over registers, which lose nothing where the mean is far from zero),
 // then the output.
-template <class T, class W, int TPR, int EPT>
+template <class T, class W, int TPR, int EPT, RowKind KIND>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void ln_forward(
     const T* x, const T* residual, const W* gamma, const W* beta, T* y, T* sum_out, float* mean_out, float* rstd_out,
     int64_t rows, int n, float eps) {
@@ -18,115 +39,138 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void ln_forward(
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     if (RPB > 1 && row >= rows) return;
-    const T* xr = x + row * n;
-    float h[V][VN];
+    Packed<T> px[V], pr[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_vec(xr, (v * TPR + t) * VN, n, h[v]);
+    for (int v = 0; v < V; ++v) Cols<T, KIND>(v * TPR + t, n).load(x + row * n, n, &px[v]);
     if (residual) {
-        const T* rr = residual + row * n;
-        T* sr = sum_out + row * n;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = (v * TPR + t) * VN;
-            float r[VN];
-            load_vec(rr, c, n, r);
+        for (int v = 0; v < V; ++v) Cols<T, KIND>(v * TPR + t, n).load(residual + row * n, n, &pr[v]);
+    }
+    Params<T, W, KIND> g[V], b[V];
 #pragma unroll
-            for (int i = 0; i < VN; ++i) h[v][i] = (float)(T)(h[v][i] + r[i]);   // the sum as stored
-            store_vec(sr, c, n, h[v]);
+    for (int v = 0; v < V; ++v) {
+        const Cols<T, KIND> col(v * TPR + t, n);
+        g[v].load(gamma, col, n);
+        if (beta) b[v].load(beta, col, n);
+    }
+    float h[V][VN], s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const Cols<T, KIND> col(v * TPR + t, n);
+        if (residual) {
+#pragma unroll
+            for (int i = 0; i < VN; ++i) h[v][i] = px[v].get(i) + pr[v].get(i);
+            px[v].set(h[v]);   // the sum as stored
+            col.store(sum_out + row * n, n, px[v]);
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            h[v][i] = px[v].get(i);
+            s += col.has(i, n) ? h[v][i] : 0.0f;
         }
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < VN; ++i) s += h[v][i];
     const float mean = (TPR == 64 ? lanes_sum<64>(s) : group_sum<TPR>(s, buf[0])) / (float)n;
     float q = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        const Cols<T, KIND> col(v * TPR + t, n);
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const float d = (v * TPR + t) * VN + i < n ? h[v][i] - mean : 0.0f;
-            h[v][i] = d;
+            h[v][i] -= mean;
+            const float d = col.has(i, n) ? h[v][i] : 0.0f;
             q += d * d;
         }
+    }
     const float var = (TPR == 64 ? lanes_sum<64>(q) : group_sum<TPR>(q, buf[1])) / (float)n;
     const float rstd = 1.0f / sqrtf(var + eps);
     if (t == 0) {
         mean_out[row] = mean;
         rstd_out[row] = rstd;
     }
-    T* yr = y + row * n;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int c = (v * TPR + t) * VN;
-        if (c >= n) break;
-        float g[VN], b[VN];
-        load_n<VN>(gamma, c, n, g);
-        if (beta) {
-            load_n<VN>(beta, c, n, b);
-        } else {
 #pragma unroll
-            for (int i = 0; i < VN; ++i) b[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < VN; ++i) h[v][i] = h[v][i] * rstd * g[i] + b[i];
-        store_vec(yr, c, n, h[v]);
+        for (int i = 0; i < VN; ++i) h[v][i] = h[v][i] * rstd * g[v].get(i) + (beta ? b[v].get(i) : 0.0f);
+        Packed<T> o;
+        o.set(h[v]);
+        Cols<T, KIND>(v * TPR + t, n).store(y + row * n, n, o);
     }
 }
 
+constexpr int kNormThreads = 512;   // of a backward workgroup, or a row's where that is more
+
 // Backward.  xh = (x - mean) rstd, g = dy gamma:
 //   dx = rstd (g - avg(g) - xh avg(g xh)) + dsum,  dgamma = sum dy xh,  dbeta = sum dy.
-// Workgroup b takes rows b, b + grid, ..., a thread always the same columns,
-// so the columns' sums stay in its registers over all its rows and go to the
-// workspace once, as row b of `part` (grid x 2 x n); ln_backward_sum adds
-// those rows in order.  The next row is on its way while this one is summed.
-template <class T, class W, int TPR, int EPT>
-__global__ __launch_bounds__(TPR) void ln_backward(
+// TPR threads take a row, a thread always the same columns, so the columns'
+// sums stay in its registers over all its rows.  A workgroup's groups of TPR
+// threads add theirs up at the end, and it leaves them as row b of `part`
+// (grid x 2 x n); ln_backward_sum adds those rows in order.  While a row is
+// summed the next one is on its way, into the other of two sets of registers (a
+// copy between them would wait for it).  All groups make as many steps; a row
+// past the last is the last one again, counted nowhere.
+template <class T, class W, int TPR, int EPT, RowKind KIND>
+__global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void ln_backward(
     const T* dy, const T* x, const W* gamma, const float* mean_in, const float* rstd_in, const T* dsum, T* dx,
     float* part, int64_t rows, int n) {
     constexpr int VN = kVec<T>, V = EPT / VN;
-    constexpr bool AHEAD = EPT * (int)sizeof(T) * TPR <= 32768;   // what the registers of 1024 threads hold
-    __shared__ float buf[2][2][TPR / 64];
-    const int t = threadIdx.x;
+    constexpr int THREADS = TPR < kNormThreads ? kNormThreads : TPR, GROUPS = THREADS / TPR;
+    constexpr int LEFT = GROUPS > 1 ? GROUPS / 2 : 0;   // groups whose sums go through LDS at once
+    __shared__ float buf[2][2][THREADS / 64];
+    __shared__ float sums[LEFT ? LEFT * TPR * VN * 2 : 1];
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     float dg[V][VN], db[V][VN];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < VN; ++i) dg[v][i] = db[v][i] = 0.0f;
+    // gamma stays in registers where they suffice, or comes from the cache each time
+    constexpr bool KEEP = TPR < 1024 || EPT * (int)(sizeof(T) + sizeof(W)) <= 64;
+    Params<T, W, KIND> ga[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) ga[v].load(gamma, Cols<T, KIND>(v * TPR + t, n), n);
+    auto gamma_again = [&](int v) {
+        if constexpr (KEEP)
+            ga[v].again();
+        else
+            ga[v].load(gamma, Cols<T, KIND>(v * TPR + t, n), n);
+    };
+    constexpr bool AHEAD = TPR < 1024 || EPT * (int)sizeof(T) <= 32;   // two sets of a row fit in the registers
     struct Row {
-        Packed<T> x[V], d[V], s[V];
+        Packed<T> x[V], d[V];
         float mean, rstd;
     };
-    auto load = [&](int64_t row, Row* r) {
-        r->mean = mean_in[row];
-        r->rstd = rstd_in[row];
+    auto load = [&](int64_t row, Row& r) {
+        r.mean = mean_in[row];
+        r.rstd = rstd_in[row];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * TPR + t) * VN;
-            load_raw(x + row * n, c, n, &r->x[v]);
-            load_raw(dy + row * n, c, n, &r->d[v]);
-            if (dsum) load_raw(dsum + row * n, c, n, &r->s[v]);
+            const Cols<T, KIND> col(v * TPR + t, n);
+            col.load(x + row * n, n, &r.x[v]);
+            col.load(dy + row * n, n, &r.d[v]);
         }
     };
-    Row now, next;
-    int64_t row = blockIdx.x;
-    load(row, &now);   // grid <= rows
-    for (int flip = 0; row < rows; row += gridDim.x, flip ^= 1) {
-        if (AHEAD && row + gridDim.x < rows) load(row + gridDim.x, &next);
+    auto take = [&](int64_t at, Row& r, int flip) {
+        const bool live = at < rows;
+        const int64_t row = live ? at : rows - 1;
+        Packed<T> sum[V];
+        if (AHEAD && dsum) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) Cols<T, KIND>(v * TPR + t, n).load(dsum + row * n, n, &sum[v]);
+        }
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float g[VN];
-            load_n<VN>(gamma, (v * TPR + t) * VN, n, g);
+            const Cols<T, KIND> col(v * TPR + t, n);
+            gamma_again(v);
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
-                // past n dy and gamma are 0, and so is every term
-                const float d = now.d[v].get(i), xh = (now.x[v].get(i) - now.mean) * now.rstd;
+                const float d = live && col.has(i, n) ? r.d[v].get(i) : 0.0f, xh = (r.x[v].get(i) - r.mean) * r.rstd;
                 dg[v][i] += d * xh;
                 db[v][i] += d;
-                s1 += d * g[i];
-                s2 += d * g[i] * xh;
+                // added here, or d and xh would be kept beyond the barrier for it
+                asm("" : "+v"(dg[v][i]), "+v"(db[v][i]));
+                s1 += d * ga[v].get(i);
+                s2 += d * ga[v].get(i) * xh;
             }
         }
         s1 = lanes_sum<64>(s1);
@@ -134,45 +178,101 @@ __global__ __launch_bounds__(TPR) void ln_backward(
         if constexpr (TPR > 64) {
             // two buffers in turn: one barrier a row
             if ((t & 63) == 0) {
-                buf[flip][0][t >> 6] = s1;
-                buf[flip][1][t >> 6] = s2;
+                buf[flip][0][threadIdx.x >> 6] = s1;
+                buf[flip][1][threadIdx.x >> 6] = s2;
             }
             __syncthreads();
-            s1 = buf[flip][0][0];
-            s2 = buf[flip][1][0];
+            const int w0 = group * (TPR / 64);
+            s1 = buf[flip][0][w0];
+            s2 = buf[flip][1][w0];
 #pragma unroll
             for (int w = 1; w < TPR / 64; ++w) {
-                s1 += buf[flip][0][w];
-                s2 += buf[flip][1][w];
+                s1 += buf[flip][0][w0 + w];
+                s2 += buf[flip][1][w0 + w];
             }
         }
         s1 /= (float)n;
         s2 /= (float)n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * TPR + t) * VN;
-            if (c >= n) break;
-            float g[VN], o[VN];
-            load_n<VN>(gamma, c, n, g);
+            float o[VN];
+            if (!AHEAD && dsum) Cols<T, KIND>(v * TPR + t, n).load(dsum + row * n, n, &sum[v]);
+            repack(r.x[v]);
+            repack(r.d[v]);
+            gamma_again(v);
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
-                const float xh = (now.x[v].get(i) - now.mean) * now.rstd;
-                o[i] = now.rstd * (now.d[v].get(i) * g[i] - s1 - xh * s2);
-                if (dsum) o[i] += now.s[v].get(i);
+                const float xh = (r.x[v].get(i) - r.mean) * r.rstd;
+                o[i] = r.rstd * (r.d[v].get(i) * ga[v].get(i) - s1 - xh * s2);
+                if (dsum) o[i] += sum[v].get(i);
             }
-            store_vec(dx + row * n, c, n, o);
+            Packed<T> p;
+            p.set(o);
+            if (live) Cols<T, KIND>(v * TPR + t, n).store(dx + row * n, n, p);
         }
-        if (AHEAD)
-            now = next;
-        else if (row + gridDim.x < rows)
-            load(row + gridDim.x, &now);
+    };
+    Row a, b;
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+    auto within = [&](int64_t r) { return r < rows ? r : rows - 1; };
+    if constexpr (AHEAD) {
+        load(within(row), a);
+        for (int64_t first = blockIdx.x * GROUPS; first < rows;) {   // the same for all groups
+            load(within(row + step), b);
+            take(row, a, 0);
+            row += step;
+            first += step;
+            if (first >= rows) break;
+            load(within(row + step), a);
+            take(row, b, 1);
+            row += step;
+            first += step;
+        }
+    } else {
+        for (int flip = 0; row < rows; row += step, flip ^= 1) {
+            load(row, a);
+            take(row, a, flip);
+        }
     }
+    // group g's sums onto group g - half's, halving; a vector at a time
+#pragma unroll
+    for (int half = LEFT; half > 0; half >>= 1)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float* s = sums + (group % half * TPR + t) * VN * 2;
+            __syncthreads();
+            if (group >= half && group < 2 * half) {
+#pragma unroll
+                for (int i = 0; i < VN; ++i) {
+                    s[i] = dg[v][i];
+                    s[VN + i] = db[v][i];
+                }
+            }
+            __syncthreads();
+            if (group < half) {
+#pragma unroll
+                for (int i = 0; i < VN; ++i) {
+                    dg[v][i] += s[i];
+                    db[v][i] += s[VN + i];
+                }
+            }
+        }
+    if (group > 0) return;
     float* pr = part + (int64_t)blockIdx.x * 2 * n;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int c = (v * TPR + t) * VN;
-        keep_n<VN>(pr, c, n, dg[v]);
-        keep_n<VN>(pr + n, c, n, db[v]);
+        const Cols<T, KIND> col(v * TPR + t, n);
+        if (KIND == kTiny || col.skip == 0) {
+            keep_n<VN>(pr, col.c, n, dg[v]);
+            keep_n<VN>(pr + n, col.c, n, db[v]);
+        } else if (col.skip < VN) {
+#pragma unroll
+            for (int i = 0; i < VN; ++i)
+                if (col.has(i, n)) {
+                    pr[col.c + i] = dg[v][i];
+                    pr[n + col.c + i] = db[v][i];
+                }
+        }
     }
 }
 
@@ -210,22 +310,28 @@ __global__ __launch_bounds__(256) void ln_backward_sum(const float* part, int pa
     }
 }
 
-#ifndef V_MOST
-#define V_MOST (n <= 2048 ? 1024 : 256)
-#endif
 constexpr int64_t kMaxNorm = 32768;   // elements of a row: 1024 threads of 32
 
-// Workgroups of the backward pass: one part each.
+// Workgroups of the backward pass, one part each: a CU's worth, since the parts
+// are written and read again (4096 x 8192, bf16: 256 workgroups 58-61 us, 512
+// 65-68, 128 over 90; 16000 x 1001: 27, 32).
+constexpr int64_t kMostParts = 256;
 int64_t backward_parts(int64_t rows, int64_t n) {
-    const int64_t most = V_MOST;
-    return rows < most ? rows : most;
+    const int64_t groups = n <= 1024 ? 8 : n <= 2048 ? 4 : n <= 4096 ? 2 : 1;   // rows at a time
+    const int64_t want = (rows + groups - 1) / groups;
+    return want < kMostParts ? want : kMostParts;
 }
 
-// f(threads of a row, elements of a thread).
-template <class F>
+template <RowKind K>
+using Kind = std::integral_constant<RowKind, K>;
+
+// f(threads of a row, elements of a thread, kind of the row).
+template <class T, class F>
 void by_row_size(int64_t n, F&& f) {
-    auto call = [&](auto t, auto e) { f(t, e); };
-    if (n <= 512)
+    auto call = [&](auto t, auto e) { n % kVec<T> == 0 ? f(t, e, Kind<kWhole>()) : f(t, e, Kind<kRagged>()); };
+    if (n < kVec<T>)
+        f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>(), Kind<kTiny>());
+    else if (n <= 512)
         call(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
     else if (n <= 1024)
         call(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
@@ -294,11 +400,11 @@ coc_status coc_layer_norm(const void* x, const void* residual, const void* gamma
     by_types(dt, param_dt, [&](auto t, auto w) {
         using T = decltype(t);
         using W = decltype(w);
-        by_row_size(n, [&](auto tpr, auto ept) {
+        by_row_size<T>(n, [&](auto tpr, auto ept, auto kind) {
             constexpr int TPR = decltype(tpr)::value, EPT = decltype(ept)::value;
             constexpr int threads = TPR == 64 ? 256 : TPR;
             const int64_t grid = ceil_div(rows, threads / TPR);
-            ln_forward<T, W, TPR, EPT><<<dim3((uint32_t)grid), dim3(threads), 0, stream>>>(
+            ln_forward<T, W, TPR, EPT, decltype(kind)::value><<<dim3((uint32_t)grid), dim3(threads), 0, stream>>>(
                 (const T*)x, (const T*)residual, (const W*)gamma, (const W*)beta, (T*)y, (T*)sum_out, mean, rstd, rows,
                 (int)n, eps);
         });
@@ -344,9 +450,9 @@ coc_status coc_layer_norm_backward(const void* dy, const void* x, const void* ga
         by_types(dt, param_dt, [&](auto t, auto w) {
             using T = decltype(t);
             using W = decltype(w);
-            by_row_size(n, [&](auto tpr, auto ept) {
+            by_row_size<T>(n, [&](auto tpr, auto ept, auto kind) {
                 constexpr int TPR = decltype(tpr)::value, EPT = decltype(ept)::value;
-                ln_backward<T, W, TPR, EPT><<<dim3((uint32_t)parts), dim3(TPR), 0, stream>>>(
+                ln_backward<T, W, TPR, EPT, decltype(kind)::value><<<dim3((uint32_t)parts), dim3(TPR < kNormThreads ? kNormThreads : TPR), 0, stream>>>(
                     (const T*)dy, (const T*)x, (const W*)gamma, mean, rstd, (const T*)dsum, (T*)dx, (float*)ws, rows,
                     (int)n);
             });

@@ -96,6 +96,14 @@ struct Packed {
     }
 };
 
+// Makes the compiler unpack p anew after this point instead of keeping what it
+// unpacked before it: four registers across a barrier, not eight.
+template <class T>
+__device__ __forceinline__ void repack(Packed<T>& p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("" : "+v"(p.w[i]));
+}
+
 // Row elements [c, c + kVec) at an address aligned to T only; those at or past n
 // are 0.  Global memory takes 16-byte accesses of any alignment in the
 // unaligned access mode that the HSA ABI runs in, so rows of odd length need no
@@ -166,6 +174,40 @@ __device__ __forceinline__ void store_vec(T* row, int c, int n, const float* f) 
     p.set(f);
     store_raw(row, c, n, p);
 }
+
+// The columns a thread takes as its vector `i` of a row: [c, c + kVec), of which
+// the first `skip` belong to another vector.  The row's last vector ends at its
+// end, overlapping the one before, and vectors past it are there again with
+// every column skipped: every load is whole and without a branch (a branch
+// around a load makes the compiler wait for all loads before it goes on), sums
+// leave the skipped columns out, and what is written twice is the same.
+// kWhole: n is a multiple of kVec (skip is 0 or kVec); kTiny: n < kVec (one
+// vector, loaded element by element; others are past the row).
+enum RowKind { kWhole, kRagged, kTiny };
+template <class T, RowKind KIND>
+struct Cols {
+    int c, skip;
+    __device__ __forceinline__ Cols(int i, int n) {
+        c = KIND == kTiny ? i * kVec<T> : min(i * kVec<T>, n - kVec<T>);
+        skip = KIND == kTiny ? 0 : min(i * kVec<T> - c, kVec<T>);
+    }
+    __device__ __forceinline__ void load(const T* row, int n, Packed<T>* p) const {
+        if constexpr (KIND == kTiny)
+            load_raw(row, c, n, p);
+        else
+            __builtin_memcpy(p->w, row + c, 16);
+    }
+    __device__ __forceinline__ void store(T* row, int n, const Packed<T>& p) const {
+        if constexpr (KIND == kTiny)
+            store_raw(row, c, n, p);
+        else if (skip < kVec<T>)
+            stream16(row + c, p);
+    }
+    // Whether column c + i counts here.
+    __device__ __forceinline__ bool has(int i, int n) const {
+        return KIND == kTiny ? c + i < n : KIND == kWhole ? skip == 0 : i >= skip;
+    }
+};
 
 // N elements of a parameter or sum vector, whose type U may be wider than the
 // rows' (N: a multiple or a half of kVec<U>).
