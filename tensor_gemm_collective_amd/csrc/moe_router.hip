@@ -10,7 +10,7 @@ constexpr int kMaxTopk = 16;
 constexpr int kPerLane = 8;     // experts a lane holds
 constexpr int kThreads = 256;
 constexpr int kAlone = 1024;
-constexpr int kChunk = 256;         // tokens a workgroup ranks at a time
+constexpr int kChunk = 128;         // tokens a workgroup ranks at a time
 constexpr int kWords = kChunk / 32;
 constexpr int kMostBlocks = 1024;   // runs, and workgroups
 constexpr int kLeastRun = 32;       // tokens
@@ -242,11 +242,11 @@ __device__ __forceinline__ float loss_term(float count, float prob_sum, float n)
 // One token over its LG lanes, lane l holding experts [8 l, 8 l + 8).  The lane
 // orders its keys, and each of the topk rounds takes the largest of the lanes'
 // first keys and moves the list it came from up by one.  Lane 0 writes the
-// chosen keys (0: none), the largest logit and the gates' factor; ps collects
-// the probabilities.  Returns whether the token takes part.
+// chosen keys (0: none), the largest logit and the probabilities' factor; ps
+// collects the probabilities.  Returns whether the token takes part.
 template <class T, int LG>
-__device__ __forceinline__ bool route_token(const Logits<T>& l, bool take, int lane, int experts, int topk,
-                                            int renormalize, float* ps, Key<T>* ckey, float* topv, float* factor) {
+__device__ __forceinline__ bool route_token(const Logits<T>& l, bool take, int lane, int experts, int topk, float* ps,
+                                            uint64_t* slots, float* topv, float* factor) {
     typedef Key<T> K;
     K key[kPerLane];
     float x[kPerLane];
@@ -260,10 +260,8 @@ __device__ __forceinline__ bool route_token(const Logits<T>& l, bool take, int l
     const float inv = softmax_parts<LG>(x, top, live);
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) ps[i] = fmaf(x[i], inv, ps[i]);
-    float chosen = 0.0f;
     for (int j = 0;;) {
-        if (lane == 0) ckey[j] = live ? best : 0;
-        if (renormalize && best > kNone<T>) chosen += exp_below(key_logit<T>(best), top);
+        if (lane == 0) slots[j] = live ? best : 0;
         if (++j == topk) break;
         if (key[0] == best) {
 #pragma unroll
@@ -274,15 +272,35 @@ __device__ __forceinline__ bool route_token(const Logits<T>& l, bool take, int l
     }
     if (lane == 0) {
         *topv = top;
-        // where the largest logit is not finite, inv is NaN and the gates are
-        *factor = renormalize ? 1.0f / chosen + (inv - inv) : inv;
+        *factor = inv;
     }
     return live;
 }
 
+// Turns a choice's slot from its key into expert + 1 and exp(logit - top), 0
+// for none.  Returns the expert, or -1.
 template <class T>
-__device__ __forceinline__ float gate_of(Key<T> k, float top, float factor) {
-    return k > kNone<T> ? exp_below(key_logit<T>(k), top) * factor : 0.0f;
+__device__ __forceinline__ int open_slot(uint64_t* slot, float top) {
+    const Key<T> k = (Key<T>)*slot;
+    if (k <= kNone<T>) {
+        *slot = 0;
+        return -1;
+    }
+    const int e = key_expert<T>(k);
+    *slot = (uint64_t)(e + 1) << 32 | __float_as_uint(exp_below(key_logit<T>(k), top));
+    return e;
+}
+__device__ __forceinline__ int slot_expert(uint64_t slot) { return (int)(slot >> 32) - 1; }
+
+// The gate of slot j of a token's topk.  Where the largest logit is not finite
+// the factor is NaN, and so are the gates.
+__device__ __forceinline__ float gate_of(const uint64_t* slots, int j, int topk, float factor, int renormalize) {
+    if (slots[j] == 0) return 0.0f;
+    const float e = __uint_as_float((uint32_t)slots[j]);
+    if (!renormalize) return e * factor;
+    float sum = 0.0f;
+    for (int i = 0; i < topk; ++i) sum += __uint_as_float((uint32_t)slots[i]);
+    return e / sum + (factor - factor);
 }
 
 // The number of bits of a row of words in [from, to).
@@ -328,10 +346,9 @@ template <class T, int LG, bool EIGHTS>
 __global__ __launch_bounds__(kThreads) void route_runs(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
                                                        int experts, int topk, int renormalize, RouterOut out) {
     constexpr int GROUPS = kThreads / LG;
-    typedef Key<T> K;
     extern __shared__ uint64_t lds[];
-    K* ckey = (K*)lds;                                       // kChunk x topk: the chosen keys
-    uint32_t* bits = (uint32_t*)(ckey + kChunk * topk);      // experts x kWords
+    uint64_t* slots = lds;                                   // kChunk x topk: the choices
+    uint32_t* bits = (uint32_t*)(slots + kChunk * topk);     // experts x kWords
     int32_t* seen = (int32_t*)(bits + experts * kWords);     // experts: choices of earlier chunks
     float* tops = (float*)(seen + experts);                  // kChunk: a token's largest logit
     float* factors = tops + kChunk;                          // kChunk
@@ -360,32 +377,23 @@ __global__ __launch_bounds__(kThreads) void route_runs(const T* logits, int64_t 
             const Logits<T> l = next;
             const bool take = valid;
             if (tl + GROUPS < len) fetch(tl + GROUPS);   // the next token's logits are on their way meanwhile
-            const bool live = route_token<T, LG>(l, take, lane, experts, topk, renormalize, ps, ckey + tl * topk,
-                                                 tops + tl, factors + tl);
+            const bool live =
+                route_token<T, LG>(l, take, lane, experts, topk, ps, slots + tl * topk, tops + tl, factors + tl);
             if (lane == 0) mine += live;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < len * topk; i += kThreads) {
             const int tl = (int)(((float)i + 0.5f) * per_topk);   // i / topk: i is small
-            const K k = ckey[i];
-            int e = -1;
-            if (k > kNone<T>) {
-                e = key_expert<T>(k);
-                atomicOr(&bits[e * kWords + (tl >> 5)], 1u << (tl & 31));
-            }
+            const int e = open_slot<T>(slots + i, tops[tl]);
+            if (e >= 0) atomicOr(&bits[e * kWords + (tl >> 5)], 1u << (tl & 31));
             out.ids[(int64_t)c0 * topk + i] = e;
-            out.gates[(int64_t)c0 * topk + i] = gate_of<T>(k, tops[tl], factors[tl]);
         }
         __syncthreads();
         for (int i = threadIdx.x; i < len * topk; i += kThreads) {
-            const int tl = (int)(((float)i + 0.5f) * per_topk);
-            const K k = ckey[i];
-            int rank = -1;
-            if (k > kNone<T>) {
-                const int e = key_expert<T>(k);
-                rank = seen[e] + count_bits(bits + e * kWords, 0, tl);
-            }
-            out.positions[(int64_t)c0 * topk + i] = rank;
+            const int tl = (int)(((float)i + 0.5f) * per_topk), e = slot_expert(slots[i]);
+            out.gates[(int64_t)c0 * topk + i] =
+                gate_of(slots + tl * topk, i - tl * topk, topk, factors[tl], renormalize);
+            out.positions[(int64_t)c0 * topk + i] = e < 0 ? -1 : seen[e] + count_bits(bits + e * kWords, 0, tl);
         }
         __syncthreads();
         for (int e = threadIdx.x; e < experts; e += kThreads) seen[e] += count_bits(bits + e * kWords, 0, len);
@@ -410,12 +418,11 @@ template <class T, int LG>
 __global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
                                                       int experts, int world, int topk, int renormalize, float coef,
                                                       RouterOut out) {
-    typedef Key<T> K;
     extern __shared__ uint64_t lds[];
     const int tokens = runs.tokens, pieces = runs.pieces;
     const int words = (tokens + 31) >> 5;
-    K* ckey = (K*)lds;                                              // tokens x topk
-    uint32_t* bits = (uint32_t*)(ckey + tokens * topk);             // experts x words
+    uint64_t* slots = lds;                                          // tokens x topk
+    uint32_t* bits = (uint32_t*)(slots + tokens * topk);            // experts x words
     float* tops = (float*)(bits + experts * words);                 // tokens
     float* factors = tops + tokens;                                 // tokens
     int32_t* cnt = (int32_t*)(factors + tokens);                    // pieces x experts
@@ -438,20 +445,13 @@ __global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t l
     for (int i = 0; i < kPerLane; ++i) ps[i] = 0.0f;
     bool live = false;
     if (tl < tokens)
-        live = route_token<T, LG>(l, valid, lane, experts, topk, renormalize, ps, ckey + tl * topk, tops + tl,
-                                  factors + tl);
+        live = route_token<T, LG>(l, valid, lane, experts, topk, ps, slots + tl * topk, tops + tl, factors + tl);
     __syncthreads();
     if (lane == 0 && live) atomicAdd(&taken, 1);
     for (int i = threadIdx.x; i < tokens * topk; i += kAlone) {
-        const int t = i / topk;
-        const K k = ckey[i];
-        int e = -1;
-        if (k > kNone<T>) {
-            e = key_expert<T>(k);
-            atomicOr(&bits[e * words + (t >> 5)], 1u << (t & 31));
-        }
+        const int t = i / topk, e = open_slot<T>(slots + i, tops[t]);
+        if (e >= 0) atomicOr(&bits[e * words + (t >> 5)], 1u << (t & 31));
         out.ids[i] = e;
-        out.gates[i] = gate_of<T>(k, tops[t], factors[t]);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < pieces * experts; i += kAlone) {
@@ -479,15 +479,14 @@ __global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t l
                        [&](int p, int e, int32_t r) { row[p * experts + e] = r; });
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * topk; i += kAlone) {
-        const int t = i / topk;
-        const K k = ckey[i];
+        const int t = i / topk, e = slot_expert(slots[i]);
         int at = -1;
-        if (k > kNone<T>) {
+        if (e >= 0) {
             int q = 0;
             while (t >= runs.piece_begin(q + 1)) ++q;
-            const int e = key_expert<T>(k);
             at = row[q * experts + e] + count_bits(bits + e * words, runs.piece_begin(q), t);
         }
+        out.gates[i] = gate_of(slots + t * topk, i - t * topk, topk, factors[t], renormalize);
         out.positions[i] = at;
     }
 }
@@ -612,38 +611,65 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 }
 
 // dlogits = p (a - <p, a>) + the gates' term, a_e the loss's derivative by p_e
-// with the counts held fixed, for LG lanes a token.
+// with the counts held fixed, for LG lanes a token.  The token's choices are
+// shared out over its lanes; what a choice adds goes to the lane that holds its
+// expert through LDS, where a token's lanes (one wave) keep 8 LG zeros.
 template <class T, int LG, bool EIGHTS>
 __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int64_t ld, const uint8_t* mask,
                                                            const int32_t* ids, const float* gates,
                                                            const int64_t* counts, const int64_t* valid,
                                                            const float* dgates, const float* dloss, T* dlogits,
-                                                           int64_t ld_out, int64_t tokens, int experts, int pieces,
+                                                           int64_t ld_out, int tokens, int experts, int pieces,
                                                            int topk, float coef, int renormalize) {
     constexpr int GROUPS = kThreads / LG;
+    __shared__ float extra[GROUPS][LG * kPerLane];
+    __shared__ float da[LG * kPerLane];
     const int group = threadIdx.x / LG, lane = threadIdx.x % LG;
     const int e0 = lane * kPerLane;
-    float a[kPerLane];
+    const int step = gridDim.x * GROUPS;
+    int t = blockIdx.x * GROUPS + group;
+    Logits<T> next;
+    int id0 = -1;              // the lane's first choice
+    float gate0 = 0.0f, dgate0 = 0.0f;
+    bool take = false;
+    auto fetch = [&](int at) {
+        load_logits<EIGHTS>(logits + at * ld, e0, experts, &next);
+        take = !mask || mask[at] != 0;
+        if (dgates && lane < topk) {
+            const int64_t o = (int64_t)at * topk + lane;
+            id0 = ids[o];
+            gate0 = gates[o];
+            dgate0 = dgates[o];
+        }
+    };
+    if (t < tokens) fetch(t);
     const float n = (float)(valid[0] > 0 ? valid[0] : 1);
     const float w = dloss ? dloss[0] * coef * (float)experts / (float)topk / n / n : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
+    for (int e = threadIdx.x; e < LG * kPerLane; e += kThreads) {
         int64_t c = 0;
-        if (e0 + i < experts)
-            for (int q = 0; q < pieces; ++q) c += counts[(int64_t)q * experts + e0 + i];
-        a[i] = w * (float)c;
+        if (e < experts)
+            for (int q = 0; q < pieces; ++q) c += counts[(int64_t)q * experts + e];
+        da[e] = w * (float)c;
     }
-    for (int64_t t = (int64_t)blockIdx.x * GROUPS + group; t < tokens; t += (int64_t)gridDim.x * GROUPS) {
-        float x[kPerLane];
-        Logits<T> l;
-        load_logits<EIGHTS>(logits + t * ld, e0, experts, &l);
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) x[i] = l.get(i);
-        uint32_t top_key = 0;   // the largest logit's order, as in make_key; NaN largest
+    for (int i = 0; i < kPerLane; ++i) extra[group][e0 + i] = 0.0f;
+    __syncthreads();
+    float a[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) a[i] = da[e0 + i];
+    for (; t < tokens; t += step) {
+        float x[kPerLane];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) x[i] = next.get(i);
+        const int id = id0;
+        const float gate = gate0, dgate = dgate0;
+        const bool wanted = take;
+        if (t + step < tokens) fetch(t + step);
+        uint32_t top_key = 0;   // the largest logit's order, as in make_keys; NaN largest
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) top_key = max(top_key, order_bits(x[i]));
         top_key = lanes_max<LG>(top_key);
-        const bool live = (!mask || mask[t] != 0) && top_key > Order<float>::kNegInf;
+        const bool live = wanted && top_key > Order<float>::kNegInf;
         const float top = __uint_as_float(top_key & 0x80000000u ? top_key ^ 0x80000000u : ~top_key);
         const float inv = softmax_parts<LG>(x, top, live);
         float pa = 0.0f;
@@ -652,29 +678,35 @@ __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int6
             x[i] *= inv;
             pa += x[i] * a[i];
         }
-        pa = lanes_sum<LG>(pa);
-        float inner = 0.0f, add[kPerLane];
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) add[i] = 0.0f;
+        float off = lanes_sum<LG>(pa);
         if (dgates) {
-            for (int j = 0; j < topk; ++j)
-                if (ids[t * topk + j] >= 0) inner += gates[t * topk + j] * dgates[t * topk + j];
-            for (int j = 0; j < topk; ++j) {
-                const int e = ids[t * topk + j];
-                if (e < 0) continue;
-                const float g = gates[t * topk + j] * (dgates[t * topk + j] - (renormalize ? inner : 0.0f));
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i)
-                    if (e0 + i == e) add[i] += g;
-            }
+            const int64_t o = (int64_t)t * topk;
+            float inner = id >= 0 ? gate * dgate : 0.0f;
+            for (int j = lane + LG; j < topk; j += LG)
+                if (ids[o + j] >= 0) inner += gates[o + j] * dgates[o + j];
+            inner = lanes_sum<LG>(inner);
+            const float less = renormalize ? inner : 0.0f;
+            if (!renormalize) off += inner;
+            if (id >= 0) extra[group][id] = gate * (dgate - less);
+            for (int j = lane + LG; j < topk; j += LG)
+                if (ids[o + j] >= 0) extra[group][ids[o + j]] = gates[o + j] * (dgates[o + j] - less);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         }
-        const float off = pa + (renormalize ? 0.0f : inner);
         T* out = dlogits + t * ld_out;
-        float o[kPerLane];
+        float v[kPerLane];
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) o[i] = live ? x[i] * (a[i] - off) + add[i] : 0.0f;
+        for (int i = 0; i < kPerLane; ++i) v[i] = live ? x[i] * (a[i] - off) + extra[group][e0 + i] : 0.0f;
+        if (dgates) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < kPerLane; i += kVec<T>) store_vec(out, e0 + i, experts, &o[i]);
+            for (int i = 0; i < kPerLane; ++i) extra[group][e0 + i] = 0.0f;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+#pragma unroll
+        for (int i = 0; i < kPerLane; i += kVec<T>) store_vec(out, e0 + i, experts, &v[i]);
     }
 }
 
@@ -782,12 +814,11 @@ coc_status coc_moe_router(const void* logits, int64_t ld, const uint8_t* mask, i
     RouterOut out{ids, gates, positions, counts, prob_sums, loss, valid, w, w + blocks * experts,
                   (float*)w + 2 * blocks * experts, w + 3 * blocks * experts};
     const bool one = alone(tokens, experts, pieces);   // without tokens too, where there are few experts
-    const size_t key = dt == COC_F32 ? 8 : 4;
     by_type(dt, [&](auto t) {
         using T = decltype(t);
         if (one) {
             const size_t words = (size_t)ceil_div(tokens, 32);
-            const size_t lds = (size_t)tokens * topk * key + experts * words * 4 + (size_t)tokens * 8 +
+            const size_t lds = (size_t)tokens * topk * 8 + experts * words * 4 + (size_t)tokens * 8 +
                                (size_t)pieces * experts * 8 + kAlone / 64 * (size_t)experts * 4;
             by_experts(experts, [&](auto lg, auto) {
                 route_alone<T, decltype(lg)::value><<<dim3(1), dim3(kAlone), lds, stream>>>(
@@ -795,7 +826,7 @@ coc_status coc_moe_router(const void* logits, int64_t ld, const uint8_t* mask, i
             });
             return;
         }
-        const size_t lds = kChunk * topk * key + (size_t)experts * (kWords + 1) * 4 + kChunk * 8;
+        const size_t lds = kChunk * topk * 8 + (size_t)experts * (kWords + 1) * 4 + kChunk * 8;
         by_experts(experts, [&](auto lg, auto eights) {
             route_runs<T, decltype(lg)::value, decltype(eights)::value>
                 <<<dim3((uint32_t)blocks), dim3(kThreads), lds, stream>>>((const T*)logits, ld, mask, runs, experts,
@@ -845,9 +876,9 @@ coc_status coc_moe_router_backward(const void* logits, int64_t ld, const uint8_t
         by_experts(experts, [&](auto lg, auto eights) {
             constexpr int LG = decltype(lg)::value;
             int64_t grid = ceil_div(tokens, kThreads / LG);
-            if (grid > 2048) grid = 2048;
+            if (grid > 1024) grid = 1024;
             route_backward<T, LG, decltype(eights)::value><<<dim3((uint32_t)grid), dim3(kThreads), 0, stream>>>(
-                (const T*)logits, ld, mask, ids, gates, counts, valid, dgates, dloss, (T*)dlogits, ld_out, tokens,
+                (const T*)logits, ld, mask, ids, gates, counts, valid, dgates, dloss, (T*)dlogits, ld_out, (int)tokens,
                 experts, pieces, topk, coef, renormalize);
         });
     });

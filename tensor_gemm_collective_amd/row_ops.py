@@ -9,27 +9,43 @@ from __future__ import annotations
 
 from typing import NamedTuple
 
-from .coc import _check, _dtype_code, _ptr, _stream, lib
+import torch
+
+from .coc import _check, _dtype_code, _stream, lib
+
+# torch's own quick way to the current stream's handle; current_stream() makes an
+# object for it, which takes longer than a small kernel's launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_gpu(like):
+    if not like.is_cuda:
+        raise ValueError(f"the tensors must be on the GPU, got {like.device}")
 
 
 def _new(shape, dtype, like, stream):
     """Memory for the work that goes to `stream`: allocated on that stream, so that
     the allocator neither hands out memory that earlier work of another stream still
     uses nor takes a workspace back before the call's kernels are done with it."""
-    import torch
-    if not like.is_cuda:
-        raise ValueError(f"the tensors must be on the GPU, got {like.device}")
+    _on_gpu(like)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _queue(stream, like):
     """The handle of the stream the call's work goes to."""
-    if not like.is_cuda:
-        raise ValueError(f"the tensors must be on the GPU, got {like.device}")
+    _on_gpu(like)
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(like.device.index)
     return _stream(stream, like.device)
+
+
+def _ptr(t):
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous (row-major)")
+    return t.data_ptr()
 
 
 def _want(t, name, like, dtype, *shape):
@@ -38,7 +54,7 @@ def _want(t, name, like, dtype, *shape):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return _ptr(t)
 
@@ -56,7 +72,6 @@ def _opt(t, name, like, dtype, *shape):
 
 def _workspace(ws, need, like, stream):
     """(tensor or None, address, bytes) of a workspace of at least `need` bytes."""
-    import torch
     if ws is None:
         if not need:
             return None, None, 0
@@ -79,7 +94,6 @@ def layer_norm(x, gamma, beta=None, *, residual=None, eps=1e-5, y=None, sum_out=
     gamma, beta: n values of x's dtype or float32.  Returns (y, mean, rstd), or
     (y, mean, rstd, sum) with a residual: sum is what was normalised, the next
     residual and the x of the backward pass."""
-    import torch
     rows, n = _matrix(x, "x")
     dt, pdt = _dtype_code(x), _dtype_code(gamma)
     px, pg = _ptr(x), _want(gamma, "gamma", x, gamma.dtype, n)
@@ -99,7 +113,6 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, *, dsum=None, dx=None, dgamma=
                         stream=None):
     """Gradients of layer_norm by what it normalised (x: its input, or its sum),
     gamma and beta.  dsum (rows x n) is added to dx.  Returns (dx, dgamma, dbeta)."""
-    import torch
     rows, n = _matrix(x, "x")
     dt, pdt = _dtype_code(x), _dtype_code(gamma)
     pd, px = _want(dy, "dy", x, x.dtype, rows, n), _ptr(x)
@@ -117,7 +130,6 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, *, dsum=None, dx=None, dgamma=
 
 
 def _ids_code(ids):
-    import torch
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
     return 0 if ids.dtype == torch.int32 else 1
@@ -174,7 +186,6 @@ def _logits(t, name):
 
 
 def _mask_ptr(mask, like, tokens):
-    import torch
     if mask is None:
         return None
     if mask.dtype == torch.bool:
@@ -187,7 +198,6 @@ def moe_router(logits, topk, *, pieces=1, world=1, coef=0.01, renormalize=True, 
     """Top-k routing of logits (tokens x experts, rows may be strided) with the
     per-expert counts, the rows' places in the send order and the balance loss.
     mask: tokens bool or uint8, 0 for tokens that take no part.  Returns a Routing."""
-    import torch
     tokens, experts, ld, pl = _logits(logits, "logits")
     pm = _mask_ptr(mask, logits, tokens)
     i32, f32, i64 = torch.int32, torch.float32, torch.int64
@@ -210,7 +220,6 @@ def moe_router_backward(logits, ids, gates, counts, valid, dgates, dloss, *, coe
     """Gradient by the logits from the gates' (dgates) and the loss's (dloss, one
     float32 on the device); either may be None.  The other arguments are the
     forward's, and ids, gates, counts and valid its results."""
-    import torch
     tokens, experts, ld, pl = _logits(logits, "logits")
     topk, pieces = _matrix(ids, "ids")[1], _matrix(counts, "counts")[0]
     pm = _mask_ptr(mask, logits, tokens)
@@ -238,7 +247,6 @@ def moe_permute(x, positions, rows=None, *, out=None, stream=None):
     """out[positions[t, j]] = x[t].  rows: rows of out (default: one for each
     entry of positions); entries outside [0, rows) are skipped, and rows that
     no entry names are not written."""
-    import torch
     tokens, n = _matrix(x, "x")
     topk = _matrix(positions, "positions")[1]
     if rows is None:
@@ -252,7 +260,6 @@ def moe_permute(x, positions, rows=None, *, out=None, stream=None):
 def moe_combine(h, positions, gates=None, *, y=None, stream=None):
     """y[t] = sum over j of gates[t, j] * h[positions[t, j]] (gates None: all 1,
     the gradient of moe_permute).  Entries outside h's rows are skipped."""
-    import torch
     rows, n = _matrix(h, "h")
     tokens, topk = _matrix(positions, "positions")
     pp = _want(positions, "positions", h, torch.int32, tokens, topk)
@@ -266,7 +273,6 @@ def moe_combine(h, positions, gates=None, *, y=None, stream=None):
 def moe_combine_backward(dy, h, positions, gates, *, dh=None, dgates=None, stream=None):
     """Gradients of moe_combine: (dh, dgates).  Rows of dh that no entry of
     positions names are not written."""
-    import torch
     rows, n = _matrix(h, "h")
     tokens, topk = _matrix(positions, "positions")
     pd = _want(dy, "dy", h, h.dtype, tokens, n)
