@@ -75,7 +75,11 @@ __device__ __forceinline__ int tile_place(int r) {
 __device__ __forceinline__ int32_t tile_ranks(TileSort* s, const uint32_t* digit, const bool* valid, int bits,
                                               int32_t* rank) {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (int i = threadIdx.x; i < kWaves * kBins / 2; i += kSort) ((uint32_t*)s->wave)[i] = 0;
+    const bool bin = (int)threadIdx.x < 1 << bits;   // this thread's bin is one of the digit's
+    if (bin) {
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) s->wave[q][threadIdx.x] = 0;
+    }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -97,11 +101,15 @@ __device__ __forceinline__ int32_t tile_ranks(TileSort* s, const uint32_t* digit
     }
     __syncthreads();
     int32_t run = 0;
+    if (bin) {
+        int32_t v[kWaves];
 #pragma unroll
-    for (int q = 0; q < kWaves; ++q) {
-        const int32_t v = s->wave[q][threadIdx.x];
-        s->wave[q][threadIdx.x] = (uint16_t)run;
-        run += v;
+        for (int q = 0; q < kWaves; ++q) v[q] = s->wave[q][threadIdx.x];
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) {
+            s->wave[q][threadIdx.x] = (uint16_t)run;
+            run += v[q];
+        }
     }
     __syncthreads();
 #pragma unroll
