@@ -12,7 +12,7 @@ __device__ __forceinline__ int64_t local_row(const I* ids, int64_t t, int64_t st
 }
 
 // y[t] = scale table[id - start], or zeros.  tpr threads a token.
-template <class T, class I>
+template <class T, class I, RowKind KIND>
 __global__ __launch_bounds__(256) void embed_rows(const I* ids, const T* table, T* y, int64_t tokens, int n,
                                                   int64_t start, int64_t vocab, float scale, int tpr) {
     constexpr int VN = kVec<T>;
@@ -20,17 +20,17 @@ __global__ __launch_bounds__(256) void embed_rows(const I* ids, const T* table, 
     const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / tpr;
     if (t >= tokens) return;
     const int64_t r = local_row(ids, t, start, vocab);
-    for (int c = (int)(threadIdx.x % tpr) * VN; c < n; c += tpr * VN) {
-        float f[VN];
+    for (int v = (int)(threadIdx.x % tpr); v * VN < n; v += tpr) {
+        const Cols<T, KIND> col(v, n);
+        Packed<T> p = {};
         if (r >= 0) {
-            load_vec(table + r * n, c, n, f);
+            col.load(table + r * n, n, &p);
+            float f[VN];
 #pragma unroll
-            for (int i = 0; i < VN; ++i) f[i] = product(f[i], scale);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VN; ++i) f[i] = 0.0f;
+            for (int i = 0; i < VN; ++i) f[i] = product(p.get(i), scale);
+            p.set(f);
         }
-        store_vec(y + t * n, c, n, f);
+        col.store(y + t * n, n, p);
     }
 }
 
@@ -253,13 +253,22 @@ __global__ __launch_bounds__(kSort) void place_keys(const I* ids, const uint64_t
 constexpr int kLeastPiece = 8, kMostPiece = 64;
 constexpr int kZero = 4;       // table rows a workgroup clears
 
+// A row's columns [c, c + N), the first `skip` of which another thread writes
+// too: adding to what is there is left to that one.
 template <int N, class G>
-__device__ __forceinline__ void write_grad(G* g, int c, int n, float* acc, float scale, bool accumulate) {
+__device__ __forceinline__ void write_grad(G* g, int c, int n, float* acc, float scale, bool accumulate,
+                                           int skip = 0) {
     if (accumulate) {
         float old[N];
         load_n<N>(g, c, n, old);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = fmaf(scale, acc[i], old[i]);
+        if (skip > 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i >= skip && c + i < n) g[c + i] = (G)acc[i];
+            return;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = product(acc[i], scale);
@@ -269,7 +278,7 @@ __device__ __forceinline__ void write_grad(G* g, int c, int n, float* acc, float
 
 // The first `sums` workgroups take 256 / tpr pieces over tpr vectors of columns
 // each; the others clear the rows without tokens among kZero each.
-template <class T, class G>
+template <class T, class G, RowKind KIND>
 __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const uint8_t* flags, const T* dy, G* grad,
                                                   float* part, int plen, int64_t tokens, int n, int64_t vocab, float scale, int accumulate,
                                                   int tpr, int colblocks, int sums) {
@@ -296,11 +305,14 @@ __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const ui
     }
     __syncthreads();
     const int64_t piece = first_piece + mine;
-    const int c = ((int)(block % colblocks) * tpr + threadIdx.x % tpr) * VN;
+    const int vec = (int)(block % colblocks) * tpr + threadIdx.x % tpr;
+    if (vec * VN >= n) return;
+    const Cols<T, KIND> col(vec, n);
+    const int c = col.c;
     const uint32_t* rows = srow + 1 + mine * plen;
     const uint32_t* toks = stok + 1 + mine * plen;
     uint32_t cur = rows[0];
-    if (cur == none || c >= n) return;
+    if (cur == none) return;
     bool first = cur == rows[-1];   // the run began in the piece before
     float acc[VN];
 #pragma unroll
@@ -310,7 +322,7 @@ __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const ui
         Packed<T> v[BATCH];
 #pragma unroll
         for (int q = 0; q < BATCH; ++q)   // past the last of this rank's tokens: any row, unused
-            load_raw(dy + (int64_t)(rows[k + q] == none ? toks[0] : toks[k + q]) * n, c, n, &v[q]);
+            col.load(dy + (int64_t)(rows[k + q] == none ? toks[0] : toks[k + q]) * n, n, &v[q]);
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
             const uint32_t r = rows[k + q];
@@ -318,7 +330,7 @@ __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const ui
                 if (first)
                     keep_n<VN>(slots, c, n, acc);
                 else
-                    write_grad<VN>(grad + (int64_t)cur * n, c, n, acc, scale, accumulate);
+                    write_grad<VN>(grad + (int64_t)cur * n, c, n, acc, scale, accumulate, col.skip);
                 first = false;
                 cur = r;
 #pragma unroll
@@ -333,7 +345,7 @@ __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const ui
     if (first || cur == rows[plen])
         keep_n<VN>(slots + (first ? 0 : n), c, n, acc);
     else
-        write_grad<VN>(grad + (int64_t)cur * n, c, n, acc, scale, accumulate);
+        write_grad<VN>(grad + (int64_t)cur * n, c, n, acc, scale, accumulate, col.skip);
 }
 
 // The runs that span pieces, summed from their parts in order.  A wave looks at
@@ -450,6 +462,15 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t n) {
             ceil_div(tokens, piece_length(tokens, ceil_div(n, 8))) * 2 * n * 4};   // 8: the longest vectors, most pieces
 }
 
+// f(kind of a row of n).
+template <class T, class F>
+void by_kind(int64_t n, F&& f) {
+    if (n < kVec<T>)
+        f(std::integral_constant<RowKind, kTiny>());
+    else
+        f(std::integral_constant<RowKind, kRagged>());
+}
+
 template <class F>
 void by_type(coc_dtype dt, F&& f) {
     if (dt == COC_F32)
@@ -494,12 +515,15 @@ coc_status coc_embedding(const void* ids, coc_index id_type, const void* table, 
         using T = decltype(t);
         const int tpr = threads_per_row(ceil_div(n, kVec<T>));
         const dim3 grid((uint32_t)ceil_div(tokens, 256 / tpr));
-        if (id_type == COC_I32)
-            embed_rows<T, int32_t><<<grid, dim3(256), 0, stream>>>((const int32_t*)ids, (const T*)table, (T*)y,
-                                                                   tokens, (int)n, start, vocab, scale, tpr);
-        else
-            embed_rows<T, int64_t><<<grid, dim3(256), 0, stream>>>((const int64_t*)ids, (const T*)table, (T*)y,
-                                                                   tokens, (int)n, start, vocab, scale, tpr);
+        by_kind<T>(n, [&](auto kind) {
+            constexpr RowKind K = decltype(kind)::value;
+            if (id_type == COC_I32)
+                embed_rows<T, int32_t, K><<<grid, dim3(256), 0, stream>>>((const int32_t*)ids, (const T*)table, (T*)y,
+                                                                          tokens, (int)n, start, vocab, scale, tpr);
+            else
+                embed_rows<T, int64_t, K><<<grid, dim3(256), 0, stream>>>((const int64_t*)ids, (const T*)table, (T*)y,
+                                                                          tokens, (int)n, start, vocab, scale, tpr);
+        });
     });
     return launched("embedding");
 }
@@ -585,9 +609,12 @@ coc_status coc_embedding_grad(const void* ids, coc_index id_type, const void* dy
                 const int64_t cols = ceil_div(ceil_div(n, kVec<T>), tpr);
                 const int64_t pieces = ceil_div(ceil_div(tokens, plen), 256 / tpr);
                 const int64_t zeros = accumulate ? 0 : ceil_div(vocab, kZero);
-                sum_pieces<T, G><<<dim3((uint32_t)(pieces * cols + zeros)), dim3(256), 0, stream>>>(
-                    keys, flags, (const T*)dy, (G*)grad, part, plen, tokens, (int)n, vocab, scale, accumulate, tpr,
-                    (int)cols, (int)(pieces * cols));
+                by_kind<T>(n, [&](auto kind) {
+                    sum_pieces<T, G, decltype(kind)::value><<<dim3((uint32_t)(pieces * cols + zeros)), dim3(256), 0,
+                                                              stream>>>(
+                        keys, flags, (const T*)dy, (G*)grad, part, plen, tokens, (int)n, vocab, scale, accumulate,
+                        tpr, (int)cols, (int)(pieces * cols));
+                });
             }
         });
         const int64_t cols = ceil_div(n, 256), followed = (tokens - 1) / plen;

@@ -8,28 +8,30 @@ namespace {
 constexpr int kMaxTopk = 16;
 
 // out[positions[t][j]] = x[t].  tpr threads a token; its row is read once.
-template <class T>
+template <class T, RowKind KIND>
 __global__ __launch_bounds__(256) void permute_rows(const T* x, const int32_t* positions, T* out, int64_t tokens,
                                                     int64_t rows, int n, int topk, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
     if (t >= tokens) return;
-    for (int c = (int)(threadIdx.x % tpr) * kVec<T>; c < n; c += tpr * kVec<T>) {
+    for (int i = (int)(threadIdx.x % tpr); i * kVec<T> < n; i += tpr) {
+        const Cols<T, KIND> col(i, n);
         Packed<T> v;
-        load_raw(x + t * n, c, n, &v);
+        col.load(x + t * n, n, &v);
         for (int j = 0; j < topk; ++j) {
             const int64_t r = positions[t * topk + j];
-            if (r >= 0 && r < rows) store_raw(out + r * n, c, n, v);
+            if (r >= 0 && r < rows) col.store(out + r * n, n, v);
         }
     }
 }
 
 // y[t] = sum_j gates[t][j] h[positions[t][j]], in order of j (gates NULL: 1).
-template <class T>
+template <class T, RowKind KIND>
 __global__ __launch_bounds__(256) void combine_rows(const T* h, const int32_t* positions, const float* gates, T* y,
                                                     int64_t tokens, int64_t rows, int n, int topk, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
     if (t >= tokens) return;
-    for (int c = (int)(threadIdx.x % tpr) * kVec<T>; c < n; c += tpr * kVec<T>) {
+    for (int v = (int)(threadIdx.x % tpr); v * kVec<T> < n; v += tpr) {
+        const Cols<T, KIND> col(v, n);
         float s[kVec<T>];
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i) s[i] = 0.0f;
@@ -37,18 +39,20 @@ __global__ __launch_bounds__(256) void combine_rows(const T* h, const int32_t* p
             const int64_t r = positions[t * topk + j];
             if (r < 0 || r >= rows) continue;
             const float g = gates ? gates[t * topk + j] : 1.0f;
-            float f[kVec<T>];
-            load_vec(h + r * n, c, n, f);
+            Packed<T> f;
+            col.load(h + r * n, n, &f);
 #pragma unroll
-            for (int i = 0; i < kVec<T>; ++i) s[i] += g * f[i];
+            for (int i = 0; i < kVec<T>; ++i) s[i] += g * f.get(i);
         }
-        store_vec(y + t * n, c, n, s);
+        Packed<T> o;
+        o.set(s);
+        col.store(y + t * n, n, o);
     }
 }
 
 // dh[positions[t][j]] = gates[t][j] dy[t],  dgates[t][j] = <dy[t], h[positions[t][j]]>.
 // A wave a (token, choice).
-template <class T>
+template <class T, RowKind KIND>
 __global__ __launch_bounds__(256) void combine_backward(const T* dy, const T* h, const int32_t* positions,
                                                         const float* gates, T* dh, float* dgates, int64_t tokens,
                                                         int64_t rows, int n, int topk) {
@@ -62,16 +66,19 @@ __global__ __launch_bounds__(256) void combine_backward(const T* dy, const T* h,
     }
     const float g = gates[i];
     float s = 0.0f;
-    for (int c = lane * kVec<T>; c < n; c += 64 * kVec<T>) {
-        float d[kVec<T>], f[kVec<T>];
-        load_vec(dy + t * n, c, n, d);
-        load_vec(h + r * n, c, n, f);
+    for (int v = lane; v * kVec<T> < n; v += 64) {
+        const Cols<T, KIND> col(v, n);
+        Packed<T> d, f, o;
+        col.load(dy + t * n, n, &d);
+        col.load(h + r * n, n, &f);
+        float p[kVec<T>];
 #pragma unroll
         for (int q = 0; q < kVec<T>; ++q) {
-            s += d[q] * f[q];
-            d[q] = product(d[q], g);
+            s += col.has(q, n) ? d.get(q) * f.get(q) : 0.0f;
+            p[q] = product(d.get(q), g);
         }
-        store_vec(dh + r * n, c, n, d);
+        o.set(p);
+        col.store(dh + r * n, n, o);
     }
     s = lanes_sum<64>(s);
     if (lane == 0) dgates[i] = s;
@@ -83,14 +90,21 @@ int threads_per_row(int64_t vecs) {
     return t;
 }
 
+// f(T, kind of a row of n).
 template <class F>
-void by_type(coc_dtype dt, F&& f) {
+void by_type(coc_dtype dt, int64_t n, F&& f) {
+    auto call = [&](auto t) {
+        if (n < kVec<decltype(t)>)
+            f(t, std::integral_constant<RowKind, kTiny>());
+        else
+            f(t, std::integral_constant<RowKind, kRagged>());
+    };
     if (dt == COC_F32)
-        f(float());
+        call(float());
     else if (dt == COC_F16)
-        f(f16_t());
+        call(f16_t());
     else
-        f(bf16_t());
+        call(bf16_t());
 }
 
 coc_status check_rows(int64_t tokens, int64_t rows, int64_t n, int32_t topk, coc_dtype dt) {
@@ -125,10 +139,10 @@ coc_status coc_moe_permute(const void* x, const int32_t* positions, void* out, i
     };
     st = check_args(args, 3);
     if (st != COC_OK) return st;
-    by_type(dt, [&](auto t) {
+    by_type(dt, n, [&](auto t, auto kind) {
         using T = decltype(t);
         const int tpr = threads_per_row(ceil_div(n, kVec<T>));
-        permute_rows<T><<<dim3((uint32_t)ceil_div(tokens, 256 / tpr)), dim3(256), 0, stream>>>(
+        permute_rows<T, decltype(kind)::value><<<dim3((uint32_t)ceil_div(tokens, 256 / tpr)), dim3(256), 0, stream>>>(
             (const T*)x, positions, (T*)out, tokens, rows, (int)n, topk, tpr);
     });
     return launched("permute");
@@ -150,10 +164,10 @@ coc_status coc_moe_combine(const void* h, const int32_t* positions, const float*
     };
     st = check_args(args, 4);
     if (st != COC_OK) return st;
-    by_type(dt, [&](auto t) {
+    by_type(dt, n, [&](auto t, auto kind) {
         using T = decltype(t);
         const int tpr = threads_per_row(ceil_div(n, kVec<T>));
-        combine_rows<T><<<dim3((uint32_t)ceil_div(tokens, 256 / tpr)), dim3(256), 0, stream>>>(
+        combine_rows<T, decltype(kind)::value><<<dim3((uint32_t)ceil_div(tokens, 256 / tpr)), dim3(256), 0, stream>>>(
             (const T*)h, positions, gates, (T*)y, tokens, rows, (int)n, topk, tpr);
     });
     return launched("combine");
@@ -179,9 +193,9 @@ coc_status coc_moe_combine_backward(const void* dy, const void* h, const int32_t
     };
     st = check_args(args, 6);
     if (st != COC_OK) return st;
-    by_type(dt, [&](auto t) {
+    by_type(dt, n, [&](auto t, auto kind) {
         using T = decltype(t);
-        combine_backward<T><<<dim3((uint32_t)ceil_div(tokens * topk, 4)), dim3(256), 0, stream>>>(
+        combine_backward<T, decltype(kind)::value><<<dim3((uint32_t)ceil_div(tokens * topk, 4)), dim3(256), 0, stream>>>(
             (const T*)dy, (const T*)h, positions, gates, (T*)dh, dgates, tokens, rows, (int)n, topk);
     });
     return launched("combine backward");
