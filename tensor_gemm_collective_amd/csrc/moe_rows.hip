@@ -51,37 +51,71 @@ __global__ __launch_bounds__(256) void combine_rows(const T* h, const int32_t* p
 }
 
 // dh[positions[t][j]] = gates[t][j] dy[t],  dgates[t][j] = <dy[t], h[positions[t][j]]>.
-// A wave a (token, choice).
-template <class T, RowKind KIND>
+// TPT threads a token walk its columns, KB choices at a time: a vector of dy is
+// read once for them and their rows of h are on their way together.
+template <class T, RowKind KIND, int KB, int TPT>
 __global__ __launch_bounds__(256) void combine_backward(const T* dy, const T* h, const int32_t* positions,
                                                         const float* gates, T* dh, float* dgates, int64_t tokens,
                                                         int64_t rows, int n, int topk) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= tokens * topk) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t t = i / topk, r = positions[i];
-    if (r < 0 || r >= rows) {
-        if (lane == 0) dgates[i] = 0.0f;
-        return;
-    }
-    const float g = gates[i];
-    float s = 0.0f;
-    for (int v = lane; v * kVec<T> < n; v += 64) {
-        const Cols<T, KIND> col(v, n);
-        Packed<T> d, f, o;
-        col.load(dy + t * n, n, &d);
-        col.load(h + r * n, n, &f);
-        float p[kVec<T>];
+    __shared__ float sums[KB][4];
+    const int64_t t = (int64_t)blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
+    if (t >= tokens) return;   // a whole wave, or with TPT 256 nobody
+    const int lane = threadIdx.x % TPT;
+    for (int j0 = 0; j0 < topk; j0 += KB) {
+        int64_t r[KB];
+        float g[KB], s[KB];
+        bool ok[KB];
 #pragma unroll
-        for (int q = 0; q < kVec<T>; ++q) {
-            s += col.has(q, n) ? d.get(q) * f.get(q) : 0.0f;
-            p[q] = product(d.get(q), g);
+        for (int j = 0; j < KB; ++j) {
+            const int64_t at = t * topk + min(j0 + j, topk - 1);
+            r[j] = positions[at];
+            g[j] = gates[at];
+            const bool named = r[j] >= 0 && r[j] < rows;
+            ok[j] = named && j0 + j < topk;
+            if (!named) r[j] = 0;   // read and not used
+            s[j] = 0.0f;
         }
-        o.set(p);
-        col.store(dh + r * n, n, o);
+        if (rows > 0)
+            for (int v = lane; v * kVec<T> < n; v += TPT) {
+                const Cols<T, KIND> col(v, n);
+                Packed<T> d, f[KB];
+                col.load(dy + t * n, n, &d);
+#pragma unroll
+                for (int j = 0; j < KB; ++j) col.load(h + r[j] * n, n, &f[j]);
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    float p[kVec<T>];
+#pragma unroll
+                    for (int q = 0; q < kVec<T>; ++q) {
+                        s[j] += col.has(q, n) ? d.get(q) * f[j].get(q) : 0.0f;
+                        p[q] = product(d.get(q), g[j]);
+                    }
+                    if (ok[j]) {
+                        Packed<T> o;
+                        o.set(p);
+                        col.store(dh + r[j] * n, n, o);
+                    }
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            s[j] = lanes_sum<64>(s[j]);
+            if constexpr (TPT > 64) {
+                if ((threadIdx.x & 63) == 0) sums[j][threadIdx.x >> 6] = s[j];
+            }
+        }
+        if constexpr (TPT > 64) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < KB; ++j) s[j] = sums[j][0] + sums[j][1] + sums[j][2] + sums[j][3];
+            __syncthreads();
+        }
+        if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (j0 + j < topk) dgates[t * topk + j0 + j] = ok[j] ? s[j] : 0.0f;
+        }
     }
-    s = lanes_sum<64>(s);
-    if (lane == 0) dgates[i] = s;
 }
 
 int threads_per_row(int64_t vecs) {
@@ -96,6 +130,8 @@ void by_type(coc_dtype dt, int64_t n, F&& f) {
     auto call = [&](auto t) {
         if (n < kVec<decltype(t)>)
             f(t, std::integral_constant<RowKind, kTiny>());
+        else if (n % kVec<decltype(t)> == 0)
+            f(t, std::integral_constant<RowKind, kWhole>());
         else
             f(t, std::integral_constant<RowKind, kRagged>());
     };
@@ -195,8 +231,21 @@ coc_status coc_moe_combine_backward(const void* dy, const void* h, const int32_t
     if (st != COC_OK) return st;
     by_type(dt, n, [&](auto t, auto kind) {
         using T = decltype(t);
-        combine_backward<T, decltype(kind)::value><<<dim3((uint32_t)ceil_div(tokens * topk, 4)), dim3(256), 0, stream>>>(
-            (const T*)dy, (const T*)h, positions, gates, (T*)dh, dgates, tokens, rows, (int)n, topk);
+        auto go = [&](auto kb, auto tpt) {
+            constexpr int TPT = decltype(tpt)::value;
+            combine_backward<T, decltype(kind)::value, decltype(kb)::value, TPT>
+                <<<dim3((uint32_t)ceil_div(tokens, 256 / TPT)), dim3(256), 0, stream>>>(
+                    (const T*)dy, (const T*)h, positions, gates, (T*)dh, dgates, tokens, rows, (int)n, topk);
+        };
+        const std::integral_constant<int, 64> wave;
+        const std::integral_constant<int, 256> group;
+        const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 4> four;
+        const bool wide = ceil_div(n, kVec<T>) > 128;   // vectors enough for four waves
+        if (topk <= 2)
+            wide ? go(two, group) : go(two, wave);
+        else
+            wide ? go(four, group) : go(four, wave);
     });
     return launched("combine backward");
 }
