@@ -251,7 +251,9 @@ __global__ __launch_bounds__(kSort) void place_keys(const I* ids, const uint64_t
 // on past its piece leaves its binary32 sum in `part`: slot 0 of a piece for
 // the run it took over from the piece before, slot 1 for one that begins in it.
 constexpr int kLeastPiece = 8, kMostPiece = 64;
-constexpr int kZero = 4;       // table rows a workgroup clears
+// Table rows a workgroup clears among: 4 of 8192 columns, more of shorter ones
+// (32768 x 4096, bf16: 4 rows 171 us, 16 175, 64 188).
+int zero_rows(int64_t n) { return n >= 2048 ? 4 : (int)(n <= 8 ? 1024 : 8192 / n); }
 
 // A row's columns [c, c + N), the first `skip` of which another thread writes
 // too: adding to what is there is left to that one.
@@ -277,19 +279,21 @@ __device__ __forceinline__ void write_grad(G* g, int c, int n, float* acc, float
 }
 
 // The first `sums` workgroups take 256 / tpr pieces over tpr vectors of columns
-// each; the others clear the rows without tokens among kZero each.
+// each; the others clear the rows without tokens among `zrows` each.
 template <class T, class G, RowKind KIND>
 __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const uint8_t* flags, const T* dy, G* grad,
                                                   float* part, int plen, int64_t tokens, int n, int64_t vocab, float scale, int accumulate,
-                                                  int tpr, int colblocks, int sums) {
+                                                  int tpr, int colblocks, int sums, int zrows) {
     constexpr int VN = kVec<T>, BATCH = 8;
     __shared__ uint32_t srow[32 * kMostPiece + 2], stok[32 * kMostPiece + 2];
     if ((int)blockIdx.x >= sums) {
-        const int64_t r0 = (int64_t)((int)blockIdx.x - sums) * kZero;
+        const int64_t r0 = (int64_t)((int)blockIdx.x - sums) * zrows;
+        const int rows = (int)min((int64_t)zrows, vocab - r0), vecs = (n + kVec<G> - 1) / kVec<G>;
         const float z[kVec<G>] = {};
-        for (int64_t r = r0; r < min(r0 + kZero, vocab); ++r)
-            if (!flags[r])
-                for (int c = threadIdx.x * kVec<G>; c < n; c += 256 * kVec<G>) store_vec(grad + r * n, c, n, z);
+        for (int i = threadIdx.x; i < rows * vecs; i += 256) {
+            const int r = i / vecs;
+            if (!flags[r0 + r]) store_vec(grad + (r0 + r) * n, (i - r * vecs) * kVec<G>, n, z);
+        }
         return;
     }
     const int64_t block = blockIdx.x;
@@ -608,12 +612,12 @@ coc_status coc_embedding_grad(const void* ids, coc_index id_type, const void* dy
                 const int tpr = threads_per_row(ceil_div(n, kVec<T>));
                 const int64_t cols = ceil_div(ceil_div(n, kVec<T>), tpr);
                 const int64_t pieces = ceil_div(ceil_div(tokens, plen), 256 / tpr);
-                const int64_t zeros = accumulate ? 0 : ceil_div(vocab, kZero);
+                const int64_t zeros = accumulate ? 0 : ceil_div(vocab, zero_rows(n));
                 by_kind<T>(n, [&](auto kind) {
                     sum_pieces<T, G, decltype(kind)::value><<<dim3((uint32_t)(pieces * cols + zeros)), dim3(256), 0,
                                                               stream>>>(
                         keys, flags, (const T*)dy, (G*)grad, part, plen, tokens, (int)n, vocab, scale, accumulate,
-                        tpr, (int)cols, (int)(pieces * cols));
+                        tpr, (int)cols, (int)(pieces * cols), zero_rows(n));
                 });
             }
         });

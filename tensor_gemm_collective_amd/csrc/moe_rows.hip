@@ -150,7 +150,7 @@ coc_status check_rows(int64_t tokens, int64_t rows, int64_t n, int32_t topk, coc
         return fail(COC_ERR_SHAPE, "topk must be in [1, %d] (got %d)", kMaxTopk, topk);
     coc_status s = check_matrix(tokens, n, "the tokens' matrix");
     if (s != COC_OK) return s;
-    s = check_matrix(tokens * topk, 1, "positions");
+    s = check_matrix(tokens, topk, "positions");
     if (s != COC_OK) return s;
     return check_matrix(rows, n, "the rows' matrix");
 }

@@ -49,7 +49,7 @@ inline coc_status check_matrix(int64_t rows, int64_t cols, const char* what) {
     if (rows < 0 || cols < 0) return fail(COC_ERR_SHAPE, "%s has a negative size", what);
     if (rows >= lim || cols >= lim || rows * cols >= lim)
         return fail(COC_ERR_SHAPE, "%s has 2^31 or more elements", what);
-    if (rows >= int64_t(1) << 26) return fail(COC_ERR_SHAPE, "%s has 2^26 or more rows", what);
+    if (rows >= int64_t(1) << 25) return fail(COC_ERR_SHAPE, "%s has 2^25 or more rows", what);
     return COC_OK;
 }
 

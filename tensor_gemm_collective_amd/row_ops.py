@@ -37,6 +37,8 @@ def _new(shape, dtype, like, stream):
 def _queue(stream, like):
     """The handle of the stream the call's work goes to."""
     _on_gpu(like)
+    if like.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {like.device}, the current device is {torch.cuda.current_device()}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(like.device.index)
     return _stream(stream, like.device)

@@ -204,7 +204,8 @@ GRADS = [  # tokens, vocab, n, dtype, gradient's dtype, ids
     (32, 1, 64, "bf16", "f32", "one"), (33, 1, 64, "bf16", "bf16", "one"), (1000, 300, 515, "f32", "f32", "any"),
     (1024, 7, 40, "f16", "f16", "any"), (1025, 2000, 24, "bf16", "bf16", "skewed"), (5000, 60, 1100, "bf16", "bf16", "skewed"),
     (5000, 3, 129, "f32", "f32", "one"), (40000, 500, 16, "bf16", "f32", "skewed"), (40000, 90000, 3, "f16", "f16", "any"),
-    (3000, 1100000, 2, "f32", "f32", "any"), (2048, 1500, 33, "bf16", "bf16", "skewed"), (70, 50, 8, "bf16", "bf16", "none"), (2050, 10, 2056, "bf16", "bf16", "half"),
+    (3000, 1100000, 2, "f32", "f32", "any"), (2048, 1500, 33, "bf16", "bf16", "skewed"),
+    (10, 3000000, 1, "f32", "f32", "any"), (70, 50, 8, "bf16", "bf16", "none"), (2050, 10, 2056, "bf16", "bf16", "half"),
 ]
 
 
