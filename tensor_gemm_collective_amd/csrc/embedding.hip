@@ -11,7 +11,9 @@ __device__ __forceinline__ int64_t local_row(const I* ids, int64_t t, int64_t st
     return id >= start && id - start < vocab ? id - start : -1;   // start >= 0: no overflow
 }
 
-// y[t] = scale table[id - start], or zeros.  tpr threads a token.
+// y[t] = scale table[id - start], or zeros.  tpr threads a token.  Bound by
+// memory: 4096 tokens of 8192 of one shard in eight (bf16, 75 MB) 12-13 us, 6
+// TB/s (repeated ids are read from cache); 32768 x 4096, every id in the shard, 62 us.
 template <class T, class I, RowKind KIND>
 __global__ __launch_bounds__(256) void embed_rows(const I* ids, const T* table, T* y, int64_t tokens, int n,
                                                   int64_t start, int64_t vocab, float scale, int tpr) {
@@ -41,6 +43,9 @@ __global__ __launch_bounds__(256) void embed_rows(const I* ids, const T* table, 
 // row = vocab and come last.  A pass over more than one tile of kTile keys
 // takes two launches: the tiles' digit counts (count_digits), then every key to
 // its place (place_keys); up to one tile is sorted in a single launch (sort_tile).
+// The keys are little data, so the launches and the waits in each bound it:
+// 32768 tokens in 2 passes 4.8 + 7.4 us each, 1001 tokens 6.1 us.  (Sorted lists
+// of 1024 merged by binary search took 69 us for the same 32768.)
 constexpr int kTile = 2048;           // keys of a workgroup, two a thread
 constexpr int kSort = kTile / 2;      // its threads
 constexpr int kWaves = kSort / 64;
@@ -278,6 +283,12 @@ __device__ __forceinline__ void write_grad(G* g, int c, int n, float* acc, float
     store_n<N>(g, c, n, acc);
 }
 
+// Bound by memory: 32768 x 4096 over 32000 rows (bf16, 531 MB and 17 MB of parts)
+// 105 us, 5.2 TB/s.  Eight rows are on their way at a time; the gradient and the
+// zeros are streamed past the L2 (175 us for the whole operator with plain
+// stores, 152 with streamed ones).  The clearing workgroups come last and fill
+// the CUs that the pieces leave.
+//
 // The first `sums` workgroups take 256 / tpr pieces over tpr vectors of columns
 // each; the others clear the rows without tokens among `zrows` each.
 template <class T, class G, RowKind KIND>
@@ -355,7 +366,8 @@ __global__ __launch_bounds__(256) void sum_pieces(const uint64_t* keys, const ui
 // The runs that span pieces, summed from their parts in order.  A wave looks at
 // the run that begins in its piece and adds up to kShort parts by itself; the
 // workgroup's longer runs then go one by one to its four waves, a quarter of
-// the parts each.
+// the parts each.  Bound by three waits for memory in a row: 6.9 us of the 32768
+// tokens' 137, most of it before the first part arrives.
 constexpr int kShort = 16;
 template <class G>
 __global__ __launch_bounds__(256) void sum_parts(const uint64_t* keys, const float* part, G* grad, int plen, int64_t tokens,

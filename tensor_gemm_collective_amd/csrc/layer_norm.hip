@@ -28,7 +28,10 @@ struct Params {
 // Forward.  TPR threads hold one row in registers, EPT elements each, so a row
 // is read once: its mean, then the mean of its squared distances from it (two
 // sums over registers, which lose nothing where the mean is far from zero),
-// then the output.
+// then the output.  Bound by memory: 512 x 8192 with a residual (bf16, 33.6 MB)
+// 7.3 us, 4.6 TB/s; 16000 x 1001 with one 22 us, 5.8 TB/s; a lone row of 14336
+// 3.4 us, which is a launch and two waits.  16 values a thread: a row of 8192
+// by 512 threads took 7.2 us, by 256 threads of 32 values 11.5.
 template <class T, class W, int TPR, int EPT, RowKind KIND>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void ln_forward(
     const T* x, const T* residual, const W* gamma, const W* beta, T* y, T* sum_out, float* mean_out, float* rstd_out,
@@ -107,7 +110,9 @@ constexpr int kNormThreads = 512;   // of a backward workgroup, or a row's where
 // (grid x 2 x n); ln_backward_sum adds those rows in order.  While a row is
 // summed the next one is on its way, into the other of two sets of registers (a
 // copy between them would wait for it).  All groups make as many steps; a row
-// past the last is the last one again, counted nowhere.
+// past the last is the last one again, counted nowhere.  Bound by memory and
+// the parts: 2048 x 14336 with dsum (bf16, 235 MB and 59 MB of parts) 50.8 us,
+// 4.6 TB/s without the parts; without the second register set 87.
 template <class T, class W, int TPR, int EPT, RowKind KIND>
 __global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void ln_backward(
     const T* dy, const T* x, const W* gamma, const float* mean_in, const float* rstd_in, const T* dsum, T* dx,
@@ -278,7 +283,7 @@ __global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void ln_ba
 
 // Sums the parts' columns: 64 columns a workgroup, its four waves a quarter of
 // the parts each (in order), joined in order.  Columns [0, n) are dgamma's,
-// [n, 2n) dbeta's.
+// [n, 2n) dbeta's.  256 parts of 28672 columns, just written: 6 us, 4.9 TB/s.
 template <class W>
 __global__ __launch_bounds__(256) void ln_backward_sum(const float* part, int parts, int n, W* dgamma, W* dbeta) {
     __shared__ float buf[4][64];

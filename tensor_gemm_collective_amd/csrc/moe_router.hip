@@ -341,7 +341,11 @@ __device__ __forceinline__ void sum_probs(float* ps, float* wsum, int experts, P
 // token) in LDS, and a choice's rank among its expert's is the number of bits
 // before it, whatever order the waves ran in.  Leaves each position's rank
 // within the run, the run's counts, probability sums and number of tokens that
-// take part.
+// take part.  Bound by its instructions, not by memory: 65536 x 128 top 8 (bf16,
+// 16.8 MB of logits) 19.3 us, of which the waves issue vector instructions for
+// 10.5 (about 320 for four tokens of 16 lanes: 70 for the keys, 38 for the
+// order, 45 for the exponentials, 130 for the rounds).  Sixteen logits a lane
+// gained 1 us in bf16 and lost 6 in fp32, 32 a lane ran out of registers.
 template <class T, int LG, bool EIGHTS>
 __global__ __launch_bounds__(kThreads) void route_runs(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
                                                        int experts, int topk, int renormalize, RouterOut out) {
@@ -413,7 +417,8 @@ static_assert(kThreads / 64 <= kWords, "the waves' sums fit where the bits were"
 
 // All tokens in one workgroup and one step: LG lanes a token, at most kAlone
 // lanes.  The ranks are counted from the token's piece on, so no run ends
-// where a piece does.
+// where a piece does.  300 x 16 top 2 in 4 pieces: 8.4 us, five barriers and
+// the waits between them; the three launches of the other path took 26.
 template <class T, int LG>
 __global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t ld, const uint8_t* mask, Runs runs,
                                                       int experts, int world, int topk, int renormalize, float coef,
@@ -492,7 +497,8 @@ __global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t l
 }
 
 // One workgroup an expert, four runs a thread: each run's base, the counts and
-// the probability sums.
+// the probability sums.  128 experts of 512 runs: 4.8 us, a launch and a wait (a
+// workgroup for 16 experts, reading rows instead of columns, 12.6).
 __global__ __launch_bounds__(kMostBlocks / 4) void scan_runs(Runs runs, RouterOut out) {
     constexpr int THREADS = kMostBlocks / 4;
     __shared__ int32_t waves[THREADS / 64];
@@ -544,8 +550,8 @@ __global__ __launch_bounds__(kMostBlocks / 4) void scan_runs(Runs runs, RouterOu
 
 // Turns a run's ranks into send rows: the rows before its (piece, expert), from
 // the counts, and the choices of the piece's earlier runs.  What it reads is
-// asked for at once, so that it waits for memory once.  Workgroup 0 also writes
-// the loss and the number of tokens.
+// asked for at once, so that it waits for memory once: 6.9 us for 524288
+// choices.  Workgroup 0 also writes the loss and the number of tokens.
 __global__ __launch_bounds__(256) void place_rows(Runs runs, int experts, int world, int topk, float coef,
                                                   RouterOut out) {
     constexpr int kAhead = 4;
@@ -613,7 +619,9 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 // dlogits = p (a - <p, a>) + the gates' term, a_e the loss's derivative by p_e
 // with the counts held fixed, for LG lanes a token.  The token's choices are
 // shared out over its lanes; what a choice adds goes to the lane that holds its
-// expert through LDS, where a token's lanes (one wave) keep 8 LG zeros.
+// expert through LDS, where a token's lanes (one wave) keep 8 LG zeros.  Bound by
+// memory and the waits at its ends: 65536 x 64 top 4 (fp32, 36.8 MB) 11 us, 3.3
+// TB/s; with every lane reading every choice 18.
 template <class T, int LG, bool EIGHTS>
 __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int64_t ld, const uint8_t* mask,
                                                            const int32_t* ids, const float* gates,
