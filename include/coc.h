@@ -404,7 +404,7 @@ coc_status coc_matmul_all_reduce_w8a16(const void* x_f16, const int8_t* w_q, con
  * row-major unless a row stride is an argument.
  *
  * Unlike the matmul/collective ops, these take any sizes (odd ones too; each
- * matrix below 2^31 elements and 2^25 rows) and any element-aligned pointer.
+ * matrix below 2^31 elements, 2^25 rows and 2^30 columns) and any element-aligned pointer.
  * All their work goes to `stream` as plain kernel launches: any number of
  * them may be captured into one graph, replayed, and called from several
  * threads; a workspace belongs to one call at a time.  Sums, statistics and

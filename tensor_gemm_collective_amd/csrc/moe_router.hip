@@ -7,13 +7,15 @@ namespace {
 
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopk = 16;
-constexpr int kPerLane = 8;     // experts a lane holds
-constexpr int kThreads = 512;       // with runs for 512 workgroups: 65536 x 128 top 8 28.7 us, 256 and 1024 32.5, 1024 and 256 30.2
-constexpr int kAlone = 1024;
+constexpr int kPerLane = 8;         // experts a lane holds
+// Threads of a workgroup, and the most workgroups (runs): 65536 x 128 top 8
+// 28.7 us; 256 threads of 1024 workgroups 32.5, 1024 of 256 30.2.
+constexpr int kThreads = 512;
+constexpr int kMostBlocks = 512;
+constexpr int kLeastRun = 32;       // tokens of a run
+constexpr int kAlone = 1024;        // threads of the workgroup that routes alone
 constexpr int kChunk = 256;         // tokens a workgroup ranks at a time
 constexpr int kWords = kChunk / 32;
-constexpr int kMostBlocks = 512;   // runs, and workgroups
-constexpr int kLeastRun = 32;       // tokens
 
 constexpr float kLog2e = 1.44269504088896340736f;
 

@@ -43,12 +43,15 @@ inline coc_status check_args(const Arg* a, int count) {
 }
 
 // rows x cols of a matrix within the library's limits.  The row limit keeps
-// every launch below 2^32 threads (at most 64 a row where a row is short).
+// every launch below 2^32 threads (at most 64 a row where a row is short), and
+// the column limit the kernels' 32-bit column numbers, which run past a row's
+// end by a workgroup's step.
 inline coc_status check_matrix(int64_t rows, int64_t cols, const char* what) {
     const int64_t lim = int64_t(1) << 31;
     if (rows < 0 || cols < 0) return fail(COC_ERR_SHAPE, "%s has a negative size", what);
     if (rows >= lim || cols >= lim || rows * cols >= lim)
         return fail(COC_ERR_SHAPE, "%s has 2^31 or more elements", what);
+    if (cols >= int64_t(1) << 30) return fail(COC_ERR_SHAPE, "%s has rows of 2^30 or more elements", what);
     if (rows >= int64_t(1) << 25) return fail(COC_ERR_SHAPE, "%s has 2^25 or more rows", what);
     return COC_OK;
 }

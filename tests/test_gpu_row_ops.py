@@ -513,6 +513,36 @@ def test_permute_and_its_gradient_are_adjoint():
     assert (out * r).sum().item() == (x * tgc.moe_combine(r, tp)).sum().item()
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_matrices_of_more_than_4_gib():
+    """Rows whose bytes begin past 2^32, in every operator's big matrix."""
+    rows, n = 131071, 16383                     # just below 2^31 elements
+    g = torch.Generator(device="cuda").manual_seed(1)
+    line = torch.randn(2, n, generator=g, device="cuda")
+    big = torch.zeros(rows, n, device="cuda")
+    big[[70000, rows - 1]] = line
+    ids = torch.tensor([rows - 1, 70000], device="cuda")
+    equal(tgc.embedding(ids, big), line.flip(0).contiguous(), "lookup")
+    pos = torch.tensor([[rows - 1], [70000]], dtype=torch.int32, device="cuda")
+    equal(tgc.moe_combine(big, pos), line.flip(0).contiguous(), "combine")
+    big.zero_()
+    tgc.moe_permute(line, pos, out=big)
+    equal(big[[rows - 1, 70000]], line, "permute")
+    tgc.embedding_grad(ids, line, rows, grad=big)
+    equal(big[[rows - 1, 70000]], line, "embedding gradient")
+    assert not big[70001:rows - 1].any()
+    del big
+    x = torch.randn(65535, 32767, generator=g, device="cuda", dtype=torch.bfloat16)
+    ga = torch.rand(32767, generator=g, device="cuda").bfloat16()
+    y, mean, rstd = tgc.layer_norm(x, ga)
+    want = tgc.layer_norm(x[-3:].contiguous(), ga)
+    equal(y[-3:].contiguous(), want[0], "layer norm")
+    dx = tgc.layer_norm_backward(x, x, ga, mean, rstd, dx=y)[0]
+    want = tgc.layer_norm_backward(x[-3:].contiguous(), x[-3:].contiguous(), ga, mean[-3:].contiguous(),
+                                   rstd[-3:].contiguous())[0]
+    equal(dx[-3:].contiguous(), want, "layer norm backward")
+
+
 # ------------------------------------------------------------------ streams and graphs
 def whole_pass(s):
     """Every operator once, each on the one before's results."""

@@ -100,6 +100,7 @@ CASES = [
     (emb, dict(it=2), DTYPE), (emb, dict(dt=-1), DTYPE), (emb, dict(n=0), SHAPE), (emb, dict(start=-1), SHAPE),
     (emb, dict(vocab=1 << 26, n=1), SHAPE), (emb, dict(tokens=1 << 25), SHAPE), (emb, dict(ids=at(0) + 4), ALIGN),
     (emb, dict(y=at(1) + 16), ALIAS), (emb, dict(y=at(0)), ALIAS),
+    (emb, dict(n=1 << 30, tokens=1, vocab=1), SHAPE), (permute, dict(n=1 << 30, tokens=1, rows=1), SHAPE),
     *[(embg, {k: None}, NULL) for k in ("ids", "dy", "grad")],
     (embg, dict(ws=None), WORKSPACE), (embg, dict(nws=100), WORKSPACE), (embg, dict(ws=at(3) + 4), ALIGN),
     (embg, dict(gdt=1), DTYPE), (embg, dict(dt=0, gdt=2), DTYPE), (embg, dict(grad=at(1)), ALIAS),
