@@ -407,7 +407,8 @@ coc_status coc_matmul_all_reduce_w8a16(const void* x_f16, const int8_t* w_q, con
  * matrix below 2^31 elements, 2^25 rows and 2^30 columns) and any element-aligned pointer.
  * All their work goes to `stream` as plain kernel launches: any number of
  * them may be captured into one graph, replayed, and called from several
- * threads; a workspace belongs to one call at a time.  Sums, statistics and
+ * threads; a workspace belongs to one call at a time, and may be NULL where
+ * its size function returns 0.  Sums, statistics and
  * gates are binary32; results are rounded once, to nearest even.  The bits
  * of every result depend on the inputs and sizes alone (no floating-point
  * atomics).  Outputs must not overlap inputs or each other.  A NULL pointer
