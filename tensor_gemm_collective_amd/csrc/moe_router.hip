@@ -147,12 +147,14 @@ __device__ __forceinline__ float exp_below(float x, float top) {
 
 // x becomes exp(x - top).  Returns the factor that makes them
 // probabilities: 0 for a token that takes no part, NaN where the largest logit
-// is not finite.
+// is not finite.  A token that takes no part counts as one of -inf alone,
+// whatever it holds: its exponentials are 0, so that 0 times them is.
 template <int LG>
 __device__ __forceinline__ float softmax_parts(float* x, float top, bool live) {
+    if (!live) top = -INFINITY;
     float c = top * kLog2e;
     if (__any(!(fabsf(top) <= kHuge))) {
-        if (!(fabsf(top) < INFINITY)) {   // nothing may become NaN in a token that takes no part
+        if (!(fabsf(top) < INFINITY)) {
             c = 0.0f;
 #pragma unroll
             for (int i = 0; i < kPerLane; ++i) x[i] = -INFINITY;
