@@ -137,9 +137,12 @@ __device__ __forceinline__ void sort_keys(K* k) {
 static_assert(kPerLane == 8, "sort_keys orders 8 keys");
 
 // exp(x - top) is 2^(x log2(e) - c) with c = top log2(e) rounded: what that
-// rounding does is common to a token's experts and leaves the quotients.  Past
-// kHuge, where the product could overflow, the difference is taken first.
-constexpr float kHuge = 1e37f;
+// rounding does is common to a token's experts and leaves the quotients, as long
+// as it is small beside an exponent's range.  Up to kHuge it is at most 2^-4 (half
+// a step of c, which is below 2^21), so that the largest exponential is within 5 %
+// of 1.  Past kHuge, where it grows with the logits until every exponential
+// overflows or vanishes (from about 2^31 on), the difference is taken first.
+constexpr float kHuge = 0x1p20f;
 __device__ __forceinline__ float exp_below(float x, float top) {
     const bool huge = fabsf(top) > kHuge;
     return __builtin_amdgcn_exp2f(huge ? (x - top) * kLog2e : fmaf(x, kLog2e, -(top * kLog2e)));
