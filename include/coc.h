@@ -515,8 +515,8 @@ coc_status coc_moe_router(const void* logits, int64_t ld, const uint8_t* mask, i
  * Its gradient by the logits, given dgates (tokens x topk, optional) and
  * dloss (one binary32 value on the device, optional), with the forward's ids,
  * gates, counts and valid; the counts are constants.  Tokens that take no
- * part get zeros.  dlogits: tokens rows of `ld_out` elements, of which the
- * first `experts` are written.
+ * part get zeros; an id outside [0, experts) is no choice.  dlogits: tokens
+ * rows of `ld_out` elements, of which the first `experts` are written.
  */
 coc_status coc_moe_router_backward(const void* logits, int64_t ld, const uint8_t* mask, const int32_t* ids,
                                    const float* gates, const int64_t* counts, const int64_t* valid,

@@ -626,7 +626,8 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 // dlogits = p (a - <p, a>) + the gates' term, a_e the loss's derivative by p_e
 // with the counts held fixed, for LG lanes a token.  The token's choices are
 // shared out over its lanes; what a choice adds goes to the lane that holds its
-// expert through LDS, where a token's lanes (one wave) keep 8 LG zeros.  Bound by
+// expert through LDS, where a token's lanes (one wave) keep 8 LG zeros; an id that
+// is no expert's is no choice, and so never a place there.  Bound by
 // memory and the waits at its ends: 65536 x 64 top 4 (fp32, 36.8 MB) 11 us, 3.3
 // TB/s; with every lane reading every choice 18.
 template <class T, int LG, bool EIGHTS>
@@ -647,6 +648,7 @@ __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int6
     int id0 = -1;              // the lane's first choice
     float gate0 = 0.0f, dgate0 = 0.0f;
     bool take = false;
+    auto chosen = [&](int id) { return (uint32_t)id < (uint32_t)experts; };
     auto fetch = [&](int at) {
         load_logits<EIGHTS>(logits + at * ld, e0, experts, &next);
         take = !mask || mask[at] != 0;
@@ -696,15 +698,15 @@ __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int6
         float off = lanes_sum<LG>(pa);
         if (dgates) {
             const int64_t o = (int64_t)t * topk;
-            float inner = id >= 0 ? gate * dgate : 0.0f;
+            float inner = chosen(id) ? gate * dgate : 0.0f;
             for (int j = lane + LG; j < topk; j += LG)
-                if (ids[o + j] >= 0) inner += gates[o + j] * dgates[o + j];
+                if (chosen(ids[o + j])) inner += gates[o + j] * dgates[o + j];
             inner = lanes_sum<LG>(inner);
             const float less = renormalize ? inner : 0.0f;
             if (!renormalize) off += inner;
-            if (id >= 0) extra[group][id] = gate * (dgate - less);
+            if (chosen(id)) extra[group][id] = gate * (dgate - less);
             for (int j = lane + LG; j < topk; j += LG)
-                if (ids[o + j] >= 0) extra[group][ids[o + j]] = gates[o + j] * (dgates[o + j] - less);
+                if (chosen(ids[o + j])) extra[group][ids[o + j]] = gates[o + j] * (dgates[o + j] - less);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }

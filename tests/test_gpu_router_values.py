@@ -1,4 +1,5 @@
-"""The router's results at logits far from zero, live and masked."""
+"""The router at values that a batch seldom holds: logits far from zero, live and
+masked, and in its backward pass ids that are no expert's."""
 import numpy as np
 import pytest
 import torch
@@ -133,3 +134,25 @@ def test_router_of_logits_far_from_zero(dt, tokens, experts, topk, renormalize):
     off += spread(gates * (grel * inner + inner_off)) if renormalize else p * (rel * inner + inner_off)
     off += (40 + 2 * topk) * U * terms + least * (2 + a.max() + 2 * np.abs(dgv).max() * topk)
     within(dx, ref, off * (1 + HALF[dt]) + HALF[dt] * np.abs(ref) + TINY[dt], "dlogits")
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts,topk", [(5, 3), (12, 4), (128, 8)])   # 1, 2 and 16 lanes a token
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_backward_takes_ids_of_no_expert_as_no_choice(dt, experts, topk, renormalize):
+    tokens = 300
+    log(f"ids of no expert {dt} {experts} top {topk} renormalize={renormalize}")
+    g = torch.Generator().manual_seed(experts)
+    x = torch.randn(tokens, experts, generator=g).to(TORCH_DT[dt]).cuda()
+    r = tgc.moe_router(x, topk, renormalize=renormalize)
+    bad = torch.tensor([experts, experts + 1, 8 * ((experts + 7) // 8), 513, 70000, 2 ** 31 - 1, -2, -2 ** 31],
+                       dtype=torch.int32)
+    ids, none = r.ids.cpu(), r.ids.cpu()
+    for t in range(0, tokens, 3):
+        ids[t, t % topk] = bad[t // 3 % len(bad)]
+        none[t, t % topk] = -1
+    ids[4], none[4] = bad[:topk].repeat(2)[:topk], -1
+    dg, dl = torch.randn(tokens, topk, generator=g).cuda(), torch.ones(1, device="cuda")
+    got = tgc.moe_router_backward(x, ids.cuda(), r.gates, r.counts, r.valid, dg, dl, renormalize=renormalize)
+    want = tgc.moe_router_backward(x, none.cuda(), r.gates, r.counts, r.valid, dg, dl, renormalize=renormalize)
+    equal(got, want, "dlogits")
