@@ -8,7 +8,7 @@ namespace {
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopk = 16;
 constexpr int kPerLane = 8;         // experts a lane holds
-// Threads of a workgroup, and the most workgroups (runs): 65536 x 128 top 8
+// Threads of a forward workgroup, and the most workgroups (runs): 65536 x 128 top 8
 // 28.7 us; 256 threads of 1024 workgroups 32.5, 1024 of 256 30.2.
 constexpr int kThreads = 512;
 constexpr int kMostBlocks = 512;
@@ -628,16 +628,31 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 // shared out over its lanes; what a choice adds goes to the lane that holds its
 // expert through LDS, where a token's lanes (one wave) keep 8 LG zeros; an id that
 // is no expert's is no choice, and so never a place there.  Bound by
-// memory and the waits at its ends: 65536 x 64 top 4 (fp32, 36.8 MB) 11 us, 3.3
+// memory and the waits at its ends: 65536 x 64 top 4 (fp32, 36.8 MB) 9.1 us, 4.0
 // TB/s; with every lane reading every choice 18.
+//
+// A workgroup begins by reading the counts.  256 threads, and 512 where there are
+// more counts, for more than 128 experts (8192 x 16 top 2, fp16: 256 threads 3.2
+// us, 512 3.5; 65536 x 8 top 2, bf16: 3.6 and 3.9; 20000 x 512 top 8, bf16: 14.2 and
+// 13.6).
+constexpr int back_threads(int lanes) { return lanes > 16 ? 512 : 256; }
+// Its workgroups fill all of the GPU's threads with 16-bit logits and half of them
+// with binary32 (twice the bytes a thread has on their way); the tokens past that
+// are fetched while others are worked on.  65536 x 64 top 4, fp32: half 9.1 us, all
+// 10.5; 65536 x 128 top 8: fp32 17.3 and 20.0, bf16 11.8 and 11.0.
+template <class T>
+int64_t back_blocks(int64_t tokens, int lanes) {
+    const int threads = back_threads(lanes);
+    const int64_t most = 256 * 2048 / threads / (sizeof(T) == 4 ? 2 : 1), once = ceil_div(tokens, threads / lanes);
+    return once < most ? once : most;
+}
+
 template <class T, int LG, bool EIGHTS>
-__global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int64_t ld, const uint8_t* mask,
-                                                           const int32_t* ids, const float* gates,
-                                                           const int64_t* counts, const int64_t* valid,
-                                                           const float* dgates, const float* dloss, T* dlogits,
-                                                           int64_t ld_out, int tokens, int experts, int pieces,
-                                                           int topk, float coef, int renormalize) {
-    constexpr int GROUPS = kThreads / LG;
+__global__ __launch_bounds__(back_threads(LG)) void route_backward(
+    const T* logits, int64_t ld, const uint8_t* mask, const int32_t* ids, const float* gates, const int64_t* counts,
+    const int64_t* valid, const float* dgates, const float* dloss, T* dlogits, int64_t ld_out, int tokens, int experts,
+    int pieces, int topk, float coef, int renormalize) {
+    constexpr int THREADS = back_threads(LG), GROUPS = THREADS / LG;
     __shared__ float extra[GROUPS][LG * kPerLane];
     __shared__ float da[LG * kPerLane];
     const int group = threadIdx.x / LG, lane = threadIdx.x % LG;
@@ -662,7 +677,7 @@ __global__ __launch_bounds__(kThreads) void route_backward(const T* logits, int6
     if (t < tokens) fetch(t);
     const float n = (float)(valid[0] > 0 ? valid[0] : 1);
     const float w = dloss ? dloss[0] * coef * (float)experts / (float)topk / n / n : 0.0f;
-    for (int e = threadIdx.x; e < LG * kPerLane; e += kThreads) {
+    for (int e = threadIdx.x; e < LG * kPerLane; e += THREADS) {
         int64_t c = 0;
         if (e < experts)
             for (int q = 0; q < pieces; ++q) c += counts[(int64_t)q * experts + e];
@@ -892,9 +907,8 @@ coc_status coc_moe_router_backward(const void* logits, int64_t ld, const uint8_t
         using T = decltype(t);
         by_experts(experts, [&](auto lg, auto eights) {
             constexpr int LG = decltype(lg)::value;
-            int64_t grid = ceil_div(tokens, kThreads / LG);
-            if (grid > 1024) grid = 1024;
-            route_backward<T, LG, decltype(eights)::value><<<dim3((uint32_t)grid), dim3(kThreads), 0, stream>>>(
+            const dim3 grid((uint32_t)back_blocks<T>(tokens, LG)), threads(back_threads(LG));
+            route_backward<T, LG, decltype(eights)::value><<<grid, threads, 0, stream>>>(
                 (const T*)logits, ld, mask, ids, gates, counts, valid, dgates, dloss, (T*)dlogits, ld_out, (int)tokens,
                 experts, pieces, topk, coef, renormalize);
         });
