@@ -156,3 +156,24 @@ def test_backward_takes_ids_of_no_expert_as_no_choice(dt, experts, topk, renorma
     got = tgc.moe_router_backward(x, ids.cuda(), r.gates, r.counts, r.valid, dg, dl, renormalize=renormalize)
     want = tgc.moe_router_backward(x, none.cuda(), r.gates, r.counts, r.valid, dg, dl, renormalize=renormalize)
     equal(got, want, "dlogits")
+
+
+@pytest.mark.parametrize("tokens,experts,topk,dt", [   # more tokens than a launch holds groups of lanes
+    (70001, 64, 4, "f32"), (20003, 512, 8, "f32"), (20003, 300, 16, "bf16"), (70001, 128, 8, "f16"),
+    (600001, 7, 2, "f32")])
+def test_backward_of_many_tokens_is_that_of_its_pieces(tokens, experts, topk, dt):
+    """A token's gradient depends on its own row and the batch's sums alone: tokens taken one after another by the
+    same lanes have the bits that they have in calls of 997, where every token has its own."""
+    log(f"router backward {tokens} x {experts} top {topk} {dt}")
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    x = (2 * torch.randn(tokens, experts, generator=g, device="cuda")).to(TORCH_DT[dt])
+    mask = torch.rand(tokens, generator=g, device="cuda") > 0.1
+    dg, dl = torch.randn(tokens, topk, generator=g, device="cuda"), torch.full((1,), 3.0 * tokens, device="cuda")
+    for renormalize in (False, True):
+        r = tgc.moe_router(x, topk, renormalize=renormalize, mask=mask)
+        whole = tgc.moe_router_backward(x, r.ids, r.gates, r.counts, r.valid, dg, dl, renormalize=renormalize, mask=mask)
+        for at in [a for a in range(0, tokens, 997) if a % 7 == 0 or a > tokens - 2000]:
+            s = slice(at, at + 997)
+            part = tgc.moe_router_backward(x[s], r.ids[s], r.gates[s], r.counts, r.valid, dg[s], dl,
+                                           renormalize=renormalize, mask=mask[s])
+            equal(whole[s].contiguous(), part, f"tokens {at} on, renormalize={renormalize}")
