@@ -29,9 +29,12 @@ struct Params {
 // is read once: its mean, then the mean of its squared distances from it (two
 // sums over registers, which lose nothing where the mean is far from zero),
 // then the output.  Bound by memory: 512 x 8192 with a residual (bf16, 33.6 MB)
-// 7.3 us, 4.6 TB/s; 16000 x 1001 with one 22 us, 5.8 TB/s; a lone row of 14336
+// 7.3 us, 4.6 TB/s; 16000 x 1001 with one 21 us, 6.0 TB/s; a lone row of 14336
 // 3.4 us, which is a launch and two waits.  16 values a thread: a row of 8192
-// by 512 threads took 7.2 us, by 256 threads of 32 values 11.5.
+// by 512 threads took 7.2 us, by 256 threads of 32 values 11.5.  Rows past 16384
+// take 1024 threads of 32; with binary32 rows or parameters 4 to 32 registers of
+// them do not fit (2048 x 32768, bf16: 61 us, 4.4 TB/s; 1024 x 32768, fp32: 104
+// us, 2.6).
 template <class T, class W, int TPR, int EPT, RowKind KIND>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void ln_forward(
     const T* x, const T* residual, const W* gamma, const W* beta, T* y, T* sum_out, float* mean_out, float* rstd_out,
@@ -112,7 +115,10 @@ constexpr int kNormThreads = 512;   // of a backward workgroup, or a row's where
 // copy between them would wait for it).  All groups make as many steps; a row
 // past the last is the last one again, counted nowhere.  Bound by memory and
 // the parts: 2048 x 14336 with dsum (bf16, 235 MB and 59 MB of parts) 50.8 us,
-// 4.6 TB/s without the parts; without the second register set 87.
+// 4.6 TB/s without the parts; without the second register set 87.  1024 threads have
+// 128 registers each, too few for 16 binary32 values and their sums, or for 32 of any
+// type: 28 to 43 and 68 to 188 do not fit (1500 x 14336, fp32: 87 us, 3.0 TB/s; 2048 x
+// 32768, bf16: 224 us, 1.8).
 template <class T, class W, int TPR, int EPT, RowKind KIND>
 __global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void ln_backward(
     const T* dy, const T* x, const W* gamma, const float* mean_in, const float* rstd_in, const T* dsum, T* dx,
@@ -318,8 +324,8 @@ __global__ __launch_bounds__(256) void ln_backward_sum(const float* part, int pa
 constexpr int64_t kMaxNorm = 32768;   // elements of a row: 1024 threads of 32
 
 // Workgroups of the backward pass, one part each: a CU's worth, since the parts
-// are written and read again (4096 x 8192, bf16: 256 workgroups 58-61 us, 512
-// 65-68, 128 over 90; 16000 x 1001: 27, 32).
+// are written and read again (4096 x 8192 with dsum, bf16: 256 workgroups 61 us, 512
+// 68, 128 91; 16000 x 1001: 28, 33, 36).
 constexpr int64_t kMostParts = 256;
 int64_t backward_parts(int64_t rows, int64_t n) {
     const int64_t groups = n <= 1024 ? 8 : n <= 2048 ? 4 : n <= 4096 ? 2 : 1;   // rows at a time

@@ -349,7 +349,7 @@ __device__ __forceinline__ void sum_probs(float* ps, float* wsum, int experts, P
 // before it, whatever order the waves ran in.  Leaves each position's rank
 // within the run, the run's counts, probability sums and number of tokens that
 // take part.  Bound by its instructions, not by memory: 65536 x 128 top 8 (bf16,
-// 16.8 MB of logits) 19.3 us, of which the waves issue vector instructions for
+// 16.8 MB of logits) 19.1 us, of which the waves issue vector instructions for
 // 10.5 (about 320 for four tokens of 16 lanes: 70 for the keys, 38 for the
 // order, 45 for the exponentials, 130 for the rounds).  Sixteen logits a lane
 // gained 1 us in bf16 and lost 6 in fp32, 32 a lane ran out of registers.
@@ -504,7 +504,7 @@ __global__ __launch_bounds__(kAlone) void route_alone(const T* logits, int64_t l
 }
 
 // One workgroup an expert, four runs a thread: each run's base, the counts and
-// the probability sums.  128 experts of 512 runs: 4.8 us, a launch and a wait (a
+// the probability sums.  128 experts of 512 runs: 4.2 us, a launch and a wait (a
 // workgroup for 16 experts, reading rows instead of columns, 12.6).
 __global__ __launch_bounds__(kMostBlocks / 4) void scan_runs(Runs runs, RouterOut out) {
     constexpr int THREADS = kMostBlocks / 4;
@@ -557,7 +557,7 @@ __global__ __launch_bounds__(kMostBlocks / 4) void scan_runs(Runs runs, RouterOu
 
 // Turns a run's ranks into send rows: the rows before its (piece, expert), from
 // the counts, and the choices of the piece's earlier runs.  What it reads is
-// asked for at once, so that it waits for memory once: 6.9 us for 524288
+// asked for at once, so that it waits for memory once: 7.0 us for 524288
 // choices.  Workgroup 0 also writes the loss and the number of tokens.
 __global__ __launch_bounds__(256) void place_rows(Runs runs, int experts, int world, int topk, float coef,
                                                   RouterOut out) {

@@ -8,7 +8,7 @@ namespace {
 constexpr int kMaxTopk = 16;
 
 // out[positions[t][j]] = x[t].  tpr threads a token; its row is read once.  Bound
-// by memory: 8192 tokens x 12288 to two rows each (bf16, 604 MB) 113 us, 5.4 TB/s;
+// by memory: 8192 tokens x 12288 to two rows each (bf16, 604 MB) 112 us, 5.4 TB/s;
 // 300 x 130 3.0 us, a launch.
 template <class T, RowKind KIND>
 __global__ __launch_bounds__(256) void permute_rows(const T* x, const int32_t* positions, T* out, int64_t tokens,
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void combine_rows(const T* h, const int32_t* p
 // TPT threads a token walk its columns, KB choices at a time: a vector of dy is
 // read once for them and their rows of h are on their way together.  Bound by
 // memory: 8192 x 12288 top 2 (bf16, 1.01 GB) 191 us, 5.3 TB/s; 30000 x 1001 top 8
-// 233 us (a wave a choice: 202 and 275).
+// 238 us, 4.3 TB/s (a wave a choice: 202 and 275).
 template <class T, RowKind KIND, int KB, int TPT>
 __global__ __launch_bounds__(256) void combine_backward(const T* dy, const T* h, const int32_t* positions,
                                                         const float* gates, T* dh, float* dgates, int64_t tokens,
