@@ -152,6 +152,11 @@ typedef enum coc_quant_mode {
     COC_PER_GROUP = 2     /* one scale per (k / group, n)       */
 } coc_quant_mode;
 
+typedef enum coc_act {
+    COC_ACT_SILU = 0,     /* g / (1 + exp(-g))                                            */
+    COC_ACT_GELU = 1      /* g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))            */
+} coc_act;
+
 typedef enum coc_status {
     COC_OK = 0,
     COC_ERR_NULL = 1,       /* a required pointer is NULL                      */
@@ -546,6 +551,136 @@ coc_status coc_moe_combine(const void* h, const int32_t* positions, const float*
 coc_status coc_moe_combine_backward(const void* dy, const void* h, const int32_t* positions, const float* gates,
                                     void* dh, float* dgates, int64_t tokens, int64_t rows, int64_t n, int32_t topk,
                                     coc_dtype dt, hipStream_t stream);
+
+/*
+ * ------------------------------------------------------------------ gated feed-forward block
+ * The block around the gate/up and down matmuls: the root-mean-square norm in
+ * front of it, both projections with the activation and their product, and
+ * for serving the matrix product in 8-bit floating point.  Like the row
+ * operators above: plain kernel launches on `stream` (any number of them in
+ * one captured graph, from several threads), no floating-point atomics,
+ * binary32 sums and statistics, a workspace belonging to one call at a time
+ * and NULL where its size function returns 0, outputs not overlapping inputs
+ * or each other, NULL refused unless optional, and matrices below 2^31
+ * elements, 2^25 rows and 2^30 columns.
+ *
+ * 8-bit values are e4m3 (4 exponent and 3 mantissa bits, finite up to 448,
+ * no infinities), each block of 128 along a row with a binary32 scale:
+ *
+ *   scale = max(max |y|, 2^-96) / 448,   q = round_e4m3(y / scale),   y ~ q * scale
+ *
+ * (the quotient taken as y * (448 / max) in binary32).  A block that holds an
+ * infinity or a NaN reads back as NaN throughout.  The scales of rows are
+ * stored by column block: scales[b][row], ceil(n / 128) x rows.  Rows in 8
+ * bits have a multiple of 16 elements, and their pointers are 16-byte aligned.
+ */
+
+/*
+ * Root-mean-square norm over rows of n elements (1 <= n <= 32768):
+ *
+ *   h    = x, or round_dt(x + residual) where residual is given
+ *   rstd = 1 / sqrt(sum(h^2) / n + eps)
+ *   y    = round_dt(h * rstd * gamma)
+ *
+ * coc_rms_norm_fp8 gives h * rstd * gamma in 8 bits instead (q: rows x n, n a
+ * multiple of 16; scales as above; nothing is rounded to dt in between).
+ * x, y, residual, sum_out: rows x n of `dt`, element-aligned; gamma: n of
+ * `param_dt` (dt or COC_F32); rstd: rows, binary32.  residual is optional;
+ * where it is given sum_out receives h (the next residual, and the x of the
+ * backward pass), otherwise sum_out is not used.
+ */
+coc_status coc_rms_norm(const void* x, const void* residual, const void* gamma, void* y, void* sum_out, float* rstd,
+                        int64_t rows, int64_t n, float eps, coc_dtype dt, coc_dtype param_dt, hipStream_t stream);
+coc_status coc_rms_norm_fp8(const void* x, const void* residual, const void* gamma, void* q, float* scales,
+                            void* sum_out, float* rstd, int64_t rows, int64_t n, float eps, coc_dtype dt,
+                            coc_dtype param_dt, hipStream_t stream);
+
+/*
+ * Its backward pass, x being the h that was normalised.  With xh = x * rstd
+ * and g = dy * gamma:
+ *
+ *   dx     = round_dt(rstd * (g - xh * sum(g * xh) / n) + dsum)
+ *   dgamma = round(sum over rows of dy * xh)
+ *
+ * dsum (optional, rows x n): the gradient that reaches the sum h by the
+ * residual branch.  dgamma: n of param_dt, overwritten (zeros where rows is
+ * 0).  ws: at least coc_rms_norm_backward_workspace_bytes(rows, n), 4-byte
+ * aligned.
+ */
+size_t coc_rms_norm_backward_workspace_bytes(int64_t rows, int64_t n);
+coc_status coc_rms_norm_backward(const void* dy, const void* x, const void* gamma, const float* rstd, const void* dsum,
+                                 void* dx, void* dgamma, int64_t rows, int64_t n, coc_dtype dt, coc_dtype param_dt,
+                                 void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * x (rows x n of `dt`, element-aligned) in 8 bits: block_rows 1, scales as
+ * above; block_rows 128 (weights), a scale for each 128 x 128, scales[r][b],
+ * ceil(rows / 128) x ceil(n / 128).  block_rows is 1 or 128.
+ */
+coc_status coc_quantize_fp8(const void* x, void* q, float* scales, int64_t rows, int64_t n, int32_t block_rows,
+                            coc_dtype dt, hipStream_t stream);
+
+/*
+ * Matrix product in 8 bits, y = x w^T (m x n of `dt`):
+ *
+ *   y[i][j] = round_dt(sum over b of x_scales[b][i] * w_scales[j / 128][b] * sum over k in block b of x[i][k] * w[j][k])
+ *
+ * x: m x k with scales by rows, w: n x k (n rows of k) with a scale for each
+ * 128 x 128, both as the operators here write them; k a multiple of 16, m and
+ * n any.  x, w, ws: 16-byte aligned; y: element-aligned.  Sums are binary32.
+ * ws: at least coc_matmul_fp8_workspace_bytes(m, n, k).
+ */
+size_t coc_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
+                          int64_t m, int64_t n, int64_t k, coc_dtype dt, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+
+/*
+ * The gated activation of rows of 2f elements, gate then up (f >= 1):
+ *
+ *   coc_gated_act:          h = round_dt(act(gate) * up)
+ *   coc_gated_act_fp8:      the same in 8 bits (q: rows x f, f a multiple of 16; scales as above)
+ *   coc_gated_act_backward: dgate = round_dt(dh * up * act'(gate)), dup = round_dt(dh * act(gate))
+ *
+ * gate_up, dgate_up: rows x 2f; h, dh: rows x f, all of `dt`, element-aligned.
+ */
+coc_status coc_gated_act(const void* gate_up, void* h, int64_t rows, int64_t f, coc_act act, coc_dtype dt,
+                         hipStream_t stream);
+coc_status coc_gated_act_fp8(const void* gate_up, void* q, float* scales, int64_t rows, int64_t f, coc_act act,
+                             coc_dtype dt, hipStream_t stream);
+coc_status coc_gated_act_backward(const void* dh, const void* gate_up, void* dgate_up, int64_t rows, int64_t f,
+                                  coc_act act, coc_dtype dt, hipStream_t stream);
+
+/*
+ * Both projections, the activation and the product in one kernel:
+ *
+ *   [gate up] = x w,   h = round_dt(act(gate) * up)
+ *
+ * x: m x d; w: d x 2f, the gate columns and then the up columns (the weight of
+ * the column-parallel matmul); h: m x f.  gate_up (optional, m x 2f) receives
+ * the rounded projections for the backward pass; h is formed from the
+ * unrounded ones.  dt: bf16 or fp16; d and f multiples of 8, m any; pointers
+ * 16-byte aligned.  ws: at least coc_gated_ffn_workspace_bytes(m, d, f).
+ */
+size_t coc_gated_ffn_workspace_bytes(int64_t m, int64_t d, int64_t f);
+coc_status coc_gated_ffn(const void* x, const void* w, void* h, void* gate_up, int64_t m, int64_t d, int64_t f,
+                         coc_act act, coc_dtype dt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Its backward pass.  With [dgate dup] as coc_gated_act_backward gives it,
+ * rounded to dt:
+ *
+ *   dx = round_dt([dgate dup] w^T),   dw = round_dt(x^T [dgate dup])
+ *
+ * gate_up (optional): the forward's; where it is NULL the projections are
+ * computed again.  dx (m x d) and dw (d x 2f) are optional, either not
+ * computed where it is NULL; dw is zeros where m is 0.  ws: at least
+ * coc_gated_ffn_backward_workspace_bytes(m, d, f).
+ */
+size_t coc_gated_ffn_backward_workspace_bytes(int64_t m, int64_t d, int64_t f);
+coc_status coc_gated_ffn_backward(const void* dh, const void* x, const void* w, const void* gate_up, void* dx, void* dw,
+                                  int64_t m, int64_t d, int64_t f, coc_act act, coc_dtype dt, void* ws,
+                                  size_t ws_bytes, hipStream_t stream);
 
 /* Workspace bytes an op (a coc_op value) needs at these sizes (0 when it needs none).
  * dt is ignored for COC_OP_MATMUL_ALL_REDUCE_W8A16.  Returns 0 for invalid

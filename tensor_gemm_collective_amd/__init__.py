@@ -41,3 +41,15 @@ from .row_ops import (  # noqa: F401
     moe_combine,
     moe_combine_backward,
 )
+from .block_ops import (  # noqa: F401
+    rms_norm,
+    rms_norm_fp8,
+    rms_norm_backward,
+    quantize_fp8,
+    matmul_fp8,
+    gated_act,
+    gated_act_fp8,
+    gated_act_backward,
+    gated_ffn,
+    gated_ffn_backward,
+)

@@ -42,6 +42,11 @@ EXPORTS = (
     "coc_embedding", "coc_embedding_grad", "coc_embedding_grad_workspace_bytes",
     "coc_moe_router", "coc_moe_router_backward", "coc_moe_router_workspace_bytes",
     "coc_moe_permute", "coc_moe_combine", "coc_moe_combine_backward",
+    "coc_rms_norm", "coc_rms_norm_fp8", "coc_rms_norm_backward", "coc_rms_norm_backward_workspace_bytes",
+    "coc_quantize_fp8", "coc_matmul_fp8", "coc_matmul_fp8_workspace_bytes",
+    "coc_gated_act", "coc_gated_act_fp8", "coc_gated_act_backward",
+    "coc_gated_ffn", "coc_gated_ffn_workspace_bytes",
+    "coc_gated_ffn_backward", "coc_gated_ffn_backward_workspace_bytes",
 )
 
 
@@ -135,6 +140,16 @@ def _declare_row_ops(L) -> None:
         "coc_embedding_grad": [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _i64, f32, _i32, _i32, _i32, _vp, _sz, _vp],
         "coc_moe_router": [_vp, _i64] + [_vp] * 8 + [_i64, _i32, _i32, _i32, _i32, f32, _i32, _i32, _vp, _sz, _vp],
         "coc_moe_router_backward": [_vp, _i64] + [_vp] * 8 + [_i64, _i64, _i32, _i32, _i32, f32, _i32, _i32, _vp],
+        "coc_rms_norm": [_vp] * 6 + [_i64, _i64, f32, _i32, _i32, _vp],
+        "coc_rms_norm_fp8": [_vp] * 7 + [_i64, _i64, f32, _i32, _i32, _vp],
+        "coc_rms_norm_backward": [_vp] * 7 + [_i64, _i64, _i32, _i32, _vp, _sz, _vp],
+        "coc_quantize_fp8": [_vp] * 3 + [_i64, _i64, _i32, _i32, _vp],
+        "coc_matmul_fp8": [_vp] * 5 + [_i64, _i64, _i64, _i32, _vp, _sz, _vp],
+        "coc_gated_act": [_vp] * 2 + [_i64, _i64, _i32, _i32, _vp],
+        "coc_gated_act_fp8": [_vp] * 3 + [_i64, _i64, _i32, _i32, _vp],
+        "coc_gated_act_backward": [_vp] * 3 + [_i64, _i64, _i32, _i32, _vp],
+        "coc_gated_ffn": [_vp] * 4 + [_i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp],
+        "coc_gated_ffn_backward": [_vp] * 6 + [_i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp],
         "coc_moe_permute": [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp],
         "coc_moe_combine": [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp],
         "coc_moe_combine_backward": [_vp] * 6 + [_i64, _i64, _i64, _i32, _i32, _vp],
@@ -145,6 +160,10 @@ def _declare_row_ops(L) -> None:
         "coc_layer_norm_backward_workspace_bytes": [_i64, _i64],
         "coc_embedding_grad_workspace_bytes": [_i64, _i64, _i64],
         "coc_moe_router_workspace_bytes": [_i64, _i32, _i32],
+        "coc_rms_norm_backward_workspace_bytes": [_i64, _i64],
+        "coc_matmul_fp8_workspace_bytes": [_i64, _i64, _i64],
+        "coc_gated_ffn_workspace_bytes": [_i64, _i64, _i64],
+        "coc_gated_ffn_backward_workspace_bytes": [_i64, _i64, _i64],
     }.items():
         getattr(L, name).argtypes = args
         getattr(L, name).restype = _sz

@@ -1,0 +1,270 @@
+// The gated feed-forward block in 16 bits: h = act(x Wg) * (x Wu), and its backward
+// pass.  The gate and up weights are one d x 2f matrix, as the column-parallel matmul
+// takes them.
+#include "mm_tile.h"
+
+namespace coc {
+namespace {
+
+constexpr int64_t kCus = 256;   // of an MI355X
+
+// ------------------------------------------------------------------ joining split sums
+// Adds the splits' sums in order: h and gate_up (either may be NULL) of the gated
+// product, or the plain product's result.  Eight columns a thread.
+template <class T, bool GATED>
+__global__ __launch_bounds__(256) void mm_join(const float* part, T* c, T* gate_up, int64_t m, int n, int splits,
+                                               int act) {
+    const int per_row = n / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= m * per_row) return;
+    const int64_t row = i / per_row;
+    const int col = (int)(i - row * per_row) * 8;
+    const int64_t all = GATED ? 2 * n : n;
+    auto sum = [&](int64_t at, float* v) {
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        for (int s = 0; s < splits; ++s) {
+            const f32x4* p = (const f32x4*)(part + (s * m + row) * all + at);
+            const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += lo[e];
+                v[4 + e] += hi[e];
+            }
+        }
+    };
+    float v[8];
+    sum(col, v);
+    if constexpr (GATED) {
+        float u[8];
+        sum(n + col, u);
+        if (gate_up) {
+            store_vec(gate_up + row * 2 * n, col, n, v);
+            store_vec(gate_up + row * 2 * n + n, col, n, u);
+        }
+        if (!c) return;
+        by_act((coc_act)act, [&](auto a) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = act_value<decltype(a)::value>(v[e]) * u[e];
+        });
+    }
+    store_vec(c + row * n, col, n, v);
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void fill_zeros(T* p, int64_t vectors) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < vectors) *(u32x4*)(p + i * 8) = u32x4{0, 0, 0, 0};
+}
+
+// ------------------------------------------------------------------ which tile
+// A product's shape: m x n outputs (n: f of the gated product, whose tiles hold twice
+// as many columns of B), k long.
+struct Choice {
+    int tile;        // 0: 256 x 256, 1: 128 x 128, 2: the same split, 3 .. 5: 64, 32, 16 rows by 128, split
+    int stages;      // 64-k stages of one split
+    int splits;
+};
+
+// The largest tile that still gives most CUs one, since it reads its operands least
+// often; below that 128 x 128 tiles, two a CU, and where these are too few to go round
+// the k range is split as well.  Few rows take a tile of as few: their products are a
+// pass over the weights, in as many pieces as keep every CU loading.
+Choice choose(int64_t m, int64_t n, int64_t k, bool gated, bool ta) {
+    const int64_t cols = gated ? 2 * n : n, stages = ceil_div(k, 64);
+    const int64_t big = ceil_div(m, 256) * ceil_div(cols, 256);
+    if (m > 64 && big >= kCus * 3 / 4) return {0, (int)stages, 1};
+    const int64_t rows = m > 64 ? 128 : m > 32 || ta ? 64 : m > 16 ? 32 : 16;
+    const int64_t tiles = ceil_div(m, rows) * ceil_div(cols, 128);
+    // a split of at least four stages, and at most 2 workgroups a CU in all
+    int64_t splits = 2 * kCus / tiles;
+    if (splits > stages / 4) splits = stages / 4;
+    if (splits < 1) splits = 1;
+    const int64_t each = ceil_div(stages, splits);
+    splits = ceil_div(stages, each);
+    if (rows == 128) return {splits > 1 ? 2 : 1, (int)each, (int)splits};
+    return {rows == 64 ? 3 : rows == 32 ? 4 : 5, (int)each, (int)splits};
+}
+
+size_t part_bytes(int64_t m, int64_t n, int64_t k, bool gated, bool ta = false) {
+    const Choice c = choose(m, n, k, gated, ta);
+    return c.tile >= 2 ? (size_t)(c.splits * m * (gated ? 2 * n : n) * 4) : 0;
+}
+
+template <class Tile>
+void launch_tile(MmParams p, const Choice& c, hipStream_t stream) {
+    p.tiles_m = (int)ceil_div(p.m, Tile::BM);
+    p.tiles_n = (int)ceil_div(p.n, Tile::OUT);
+    p.stages = c.stages;
+    mm_tile<Tile><<<dim3((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)c.splits), dim3(256), 0, stream>>>(p);
+}
+
+// C = A B of these sizes by the chosen tile, joined where it is split.
+template <class T, bool TA, bool TB, bool GATED>
+coc_status product(MmParams p, hipStream_t stream) {
+    const Choice c = choose(p.m, p.n, p.k, GATED, TA);
+    switch (c.tile) {
+        case 0: launch_tile<MmTile<T, TA, TB, 8, 8, 2, 2, 2, GATED, false>>(p, c, stream); break;
+        case 1: launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, false>>(p, c, stream); break;
+        case 2: launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, true>>(p, c, stream); break;
+        case 3: launch_tile<MmTile<T, TA, TB, 4, 2, 1, 4, 3, GATED, true>>(p, c, stream); break;
+        case 4:
+            if constexpr (!TA) launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, true>>(p, c, stream);
+            break;
+        default:
+            if constexpr (!TA) launch_tile<MmTile<T, TA, TB, 1, 2, 1, 4, 4, GATED, true>>(p, c, stream);
+            break;
+    }
+    coc_status st = launched("gated feed-forward product");
+    if (st != COC_OK || c.tile < 2) return st;
+    mm_join<T, GATED><<<dim3((uint32_t)ceil_div((int64_t)p.m * (p.n / 8), 256)), dim3(256), 0, stream>>>(
+        p.part, (T*)p.c, (T*)p.gate_up, p.m, p.n, c.splits, p.act);
+    return launched("gated feed-forward join");
+}
+
+template <class F>
+coc_status by_type16(coc_dtype dt, F&& f) {
+    return dt == COC_F16 ? f(f16_t()) : f(bf16_t());
+}
+
+coc_status check_ffn(int64_t m, int64_t d, int64_t f, coc_act act, coc_dtype dt) {
+    if (dt != COC_BF16 && dt != COC_F16) return fail(COC_ERR_DTYPE, "gated feed-forward: bf16 or fp16 only");
+    if (act != COC_ACT_SILU && act != COC_ACT_GELU) return fail(COC_ERR_DTYPE, "unknown activation %d", (int)act);
+    if (d < 8 || f < 8 || d % 8 != 0 || f % 8 != 0)
+        return fail(COC_ERR_SHAPE, "d and f are positive multiples of 8 (d=%lld f=%lld)", (long long)d, (long long)f);
+    const int64_t lim = int64_t(1) << 31;
+    if (d >= lim || f >= lim / 2) return fail(COC_ERR_SHAPE, "w has 2^31 or more elements");
+    coc_status st = check_matrix(m, d, "x");
+    if (st == COC_OK) st = check_matrix(m, 2 * f, "gate_up");
+    if (st == COC_OK) st = check_matrix(d, 2 * f, "w");
+    return st;
+}
+
+MmParams operands(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t m, int64_t n, int64_t k) {
+    MmParams p{};
+    p.a = a;
+    p.b = b;
+    p.lda = lda;
+    p.ldb = ldb;
+    p.m = (int)m;
+    p.n = (int)n;
+    p.k = (int)k;
+    return p;
+}
+
+coc_status gated_product(const void* x, const void* w, void* h, void* gate_up, int64_t m, int64_t d, int64_t f,
+                         coc_act act, coc_dtype dt, void* part, hipStream_t stream) {
+    MmParams p = operands(x, d, w, 2 * f, m, f, d);
+    p.c = h;
+    p.gate_up = gate_up;
+    p.act = act;
+    p.part = (float*)part;
+    return by_type16(dt, [&](auto t) { return product<decltype(t), false, false, true>(p, stream); });
+}
+
+struct BackwardSpace {
+    size_t dgate_up, part;   // bytes: the projections' gradient, then the products' split sums
+    BackwardSpace(int64_t m, int64_t d, int64_t f) {
+        dgate_up = (size_t)round_up(m * 2 * f * 2, 256);
+        const size_t a = part_bytes(m, f, d, true), b = part_bytes(m, d, 2 * f, false),
+                     c = part_bytes(d, 2 * f, m, false, true);
+        part = a > b ? (a > c ? a : c) : (b > c ? b : c);
+    }
+};
+
+}  // namespace
+}  // namespace coc
+
+extern "C" {
+
+size_t coc_gated_ffn_workspace_bytes(int64_t m, int64_t d, int64_t f) {
+    if (m <= 0 || coc::check_ffn(m, d, f, COC_ACT_SILU, COC_BF16) != COC_OK) return 0;
+    return coc::part_bytes(m, f, d, true);
+}
+
+coc_status coc_gated_ffn(const void* x, const void* w, void* h, void* gate_up, int64_t m, int64_t d, int64_t f,
+                         coc_act act, coc_dtype dt, void* ws, size_t ws_bytes, hipStream_t stream) {
+    using namespace coc;
+    clear_error();
+    coc_status st = check_ffn(m, d, f, act, dt);
+    if (st != COC_OK) return st;
+    if (m == 0) return COC_OK;
+    const size_t need = part_bytes(m, f, d, true);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(COC_ERR_WORKSPACE, "gated feed-forward needs %zu workspace bytes (got %zu)", need,
+                    ws ? ws_bytes : (size_t)0);
+    const Arg args[] = {{x, m * d * 2, 16, false, "x"},
+                        {w, d * 2 * f * 2, 16, false, "w"},
+                        {h, m * f * 2, 16, true, "h"},
+                        {gate_up, gate_up ? m * 2 * f * 2 : 0, 16, true, "gate_up"},
+                        {ws, (int64_t)need, 16, true, "ws"}};
+    st = check_args(args, 5);
+    if (st != COC_OK) return st;
+    return gated_product(x, w, h, gate_up, m, d, f, act, dt, ws, stream);
+}
+
+size_t coc_gated_ffn_backward_workspace_bytes(int64_t m, int64_t d, int64_t f) {
+    if (m <= 0 || coc::check_ffn(m, d, f, COC_ACT_SILU, COC_BF16) != COC_OK) return 0;
+    const coc::BackwardSpace s(m, d, f);
+    return s.dgate_up + s.part;
+}
+
+coc_status coc_gated_ffn_backward(const void* dh, const void* x, const void* w, const void* gate_up, void* dx, void* dw,
+                                  int64_t m, int64_t d, int64_t f, coc_act act, coc_dtype dt, void* ws,
+                                  size_t ws_bytes, hipStream_t stream) {
+    using namespace coc;
+    clear_error();
+    coc_status st = check_ffn(m, d, f, act, dt);
+    if (st != COC_OK) return st;
+    const size_t need = coc_gated_ffn_backward_workspace_bytes(m, d, f);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(COC_ERR_WORKSPACE, "gated feed-forward backward needs %zu workspace bytes (got %zu)", need,
+                    ws ? ws_bytes : (size_t)0);
+    const int64_t weights = d * 2 * f * 2;
+    const Arg args[] = {{dh, m * f * 2, 16, false, "dh"},
+                        {x, m * d * 2, 16, false, "x"},
+                        {w, weights, 16, false, "w"},
+                        {gate_up, gate_up ? m * 2 * f * 2 : 0, 16, false, "gate_up"},
+                        {dx, dx ? m * d * 2 : 0, 16, true, "dx"},
+                        {dw, dw ? weights : 0, 16, true, "dw"},
+                        {ws, (int64_t)need, 16, true, "ws"}};
+    st = check_args(args, 7);
+    if (st != COC_OK) return st;
+    if (m == 0) {
+        // no rows: the weights' gradient is 0
+        if (!dw) return COC_OK;
+        fill_zeros<uint16_t><<<dim3((uint32_t)ceil_div(weights / 16, 256)), dim3(256), 0, stream>>>((uint16_t*)dw,
+                                                                                                 weights / 16);
+        return launched("gated feed-forward backward");
+    }
+    if (!dx && !dw) return COC_OK;
+    const BackwardSpace space(m, d, f);
+    void* const dgu = ws;
+    void* const part = (uint8_t*)ws + space.dgate_up;
+    if (!gate_up) {
+        // the projections again, where their gradient will be
+        st = gated_product(x, w, nullptr, dgu, m, d, f, act, dt, part, stream);
+        if (st != COC_OK) return st;
+    }
+    launch_gated_act_backward(dh, gate_up ? gate_up : dgu, dgu, m, f, act, dt, stream);
+    st = launched("gated feed-forward backward");
+    if (st != COC_OK) return st;
+    return by_type16(dt, [&](auto t) {
+        using T = decltype(t);
+        coc_status s = COC_OK;
+        if (dx) {
+            MmParams p = operands(dgu, 2 * f, w, 2 * f, m, d, 2 * f);
+            p.c = dx;
+            p.part = (float*)part;
+            s = product<T, false, true, false>(p, stream);
+        }
+        if (s == COC_OK && dw) {
+            MmParams p = operands(x, d, dgu, 2 * f, d, 2 * f, m);
+            p.c = dw;
+            p.part = (float*)part;
+            s = product<T, true, false, false>(p, stream);
+        }
+        return s;
+    });
+}
+
+}  // extern "C"

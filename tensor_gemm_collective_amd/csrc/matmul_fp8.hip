@@ -1,0 +1,372 @@
+// Matrix product of 8-bit floating-point operands with a scale for each block of 128:
+//   y[i][j] = sum over blocks b of  xs[b][i] ws[j / 128][b]  sum over k in b of  x[i][k] w[j][k].
+// x's scales cover 128 of a row, w's 128 x 128.
+#include "fp8.h"
+#include "lds_tile.h"
+
+namespace coc {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+struct Fp8Params {
+    const uint8_t *x, *w;
+    const float *xs, *ws;
+    void* y;
+    float* part;   // partial sums: splits x m x n
+    int m, n, k, blocks;            // blocks: of 128 along k
+    int tiles_m, tiles_n, stages;   // stages: blocks of one split
+};
+
+// 128 k of 16 x 16 outputs.
+__device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
+// One BM x BN tile.  A stage is one block of 128 k, so each MFMA gives a whole block's sum,
+// which is scaled and added to the binary32 sums by the vector units (four multiply-adds
+// for each MFMA, beside the other waves' MFMAs).  The weights are the MFMA's first
+// operand: a lane then holds one row of x in each 16 x 16 block and needs one scale for
+// it.  A lane's 32 k of a fragment are chunks g and g + 4 of a row (g: its 16-lane group)
+// for both operands; the order of k within a block is free.
+template <class T, int FI, int FJ, int WM, int WN, int S, bool PART>
+struct Fp8Tile {
+    static constexpr int NW = WM * WN, BM = WM * FI * 16, BN = WN * FJ * 16, NB = BN / kScaleBlock;
+    using A = Operand<BM, false, NW, 1>;
+    using B = Operand<BN, false, NW, 1>;
+    static constexpr int XW = BM > 64 ? BM / 64 : 1;   // waves that load x's scales; the others load w's
+    static constexpr int SCALES = (XW + 1) * 256;      // bytes: 64 a wave
+    static constexpr int SLOT = A::BYTES + B::BYTES + SCALES;
+    static constexpr int LDS = S * SLOT;
+    static constexpr int DPW = A::PER_WAVE + B::PER_WAVE + 1;
+    static constexpr bool STAGED = !PART && sizeof(T) == 2;   // rows go out through the LDS
+    static_assert(BN % kScaleBlock == 0 && kScaleBlock % (FJ * 16) == 0, "a wave's columns share a scale");
+    static_assert(XW < NW, "a wave for w's scales");
+    static_assert(!STAGED || BM * BN * 2 <= LDS, "the staged output fits in the LDS");
+
+    static __device__ __forceinline__ void run(const Fp8Params& p, uint8_t* sm) {
+        int tm, tn;
+        tile_of(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn);
+        const int m0 = tm * BM, n0 = tn * BN;
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int wm = wave / WN, wn = wave % WN;
+        const uint32_t lds0 = lds_address(sm);
+        const int stage0 = PART ? (int)blockIdx.y * p.stages : 0;
+        const int KT = min(p.stages, p.blocks - stage0);   // >= 1
+
+        A a;
+        B b;
+        a.init(p.x, p.k, stage0, lds0, wave, lane, [&](int r) { return min(m0 + r, p.m - 1); });
+        b.init(p.w, p.k, stage0, lds0 + A::BYTES, wave, lane, [&](int c) { return min(n0 + c, p.n - 1); });
+        // scales: 64 rows of x, or this tile's column blocks of w over and over
+        const bool of_x = wave < XW;
+        const uint32_t scale_off = 4u * (uint32_t)(of_x ? min(m0 + wave * 64 + lane, p.m - 1)
+                                                        : min(n0 / kScaleBlock + lane % NB, (p.n - 1) / kScaleBlock) *
+                                                              p.blocks);
+        const int64_t scale_step = of_x ? (int64_t)p.m * 4 : 4;
+        const uint8_t* scale_base = (const uint8_t*)(of_x ? p.xs : p.ws) + stage0 * scale_step;
+        const uint32_t scale_lds = lds0 + A::BYTES + B::BYTES + (of_x ? wave : XW) * 256;
+        auto load = [&](int d, int s, int slot) {
+            const int left = p.k - (stage0 + s) * kScaleBlock;
+            if (d < A::PER_WAVE)
+                a.load(d, s, slot * SLOT, left);
+            else if (d < A::PER_WAVE + B::PER_WAVE)
+                b.load(d - A::PER_WAVE, s, slot * SLOT, left);
+            else
+                load_lds4(scale_off, scale_base + s * scale_step,
+                          __builtin_amdgcn_readfirstlane(scale_lds + slot * SLOT));
+        };
+
+        const int ra = wm * FI * 16 + (lane & 15), rb = wn * FJ * 16 + (lane & 15);
+        int pa[2], pb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            pa[h] = ra * 128 + (((h * 4 + (lane >> 4)) ^ row_swizzle(ra)) << 4);
+            pb[h] = A::BYTES + rb * 128 + (((h * 4 + (lane >> 4)) ^ row_swizzle(rb)) << 4);
+        }
+        const COC_LDS uint8_t* lds = (const COC_LDS uint8_t*)sm;
+        auto fragment = [&](int at0, int at1) {
+            const u32x4 lo = *(const COC_LDS u32x4*)(lds + at0), hi = *(const COC_LDS u32x4*)(lds + at1);
+            return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4,
+                                           5, 6, 7);
+        };
+        auto read_a = [&](int slot, int i) {
+            return fragment(slot * SLOT + pa[0] + i * 2048, slot * SLOT + pa[1] + i * 2048);
+        };
+        auto read_b = [&](int slot, int j) {
+            return fragment(slot * SLOT + pb[0] + j * 2048, slot * SLOT + pb[1] + j * 2048);
+        };
+        auto read_scale = [&](int slot, int i) {
+            return *(const COC_LDS float*)(lds + slot * SLOT + A::BYTES + B::BYTES + (ra + i * 16) * 4);
+        };
+        auto read_w_scale = [&](int slot) {
+            return *(const COC_LDS float*)(lds + slot * SLOT + A::BYTES + B::BYTES + XW * 256 +
+                                           (NB > 1 ? wn * FJ * 16 / kScaleBlock * 4 : 0));
+        };
+
+        f32x4 acc[FI][FJ];
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        for (int s = 0; s < S && s < KT; ++s)
+#pragma unroll
+            for (int d = 0; d < DPW; ++d) load(d, s, s);
+        if (KT >= S)
+            wait_loads<(S - 1) * DPW>();
+        else
+            wait_loads<0>();
+        group_barrier();
+        i32x8 fa[2], fb[FJ];
+        float sx[FI], sw;
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) fb[j] = read_b(0, j);
+        fa[0] = read_a(0, 0);
+
+        // One stage.  The next row block's fragment is read under this one's MFMAs; before
+        // the last row block the workgroup meets (every wave has read this slot, and the
+        // next stage has arrived), and under its MFMAs the next stage's first fragments are
+        // read and stage kt + S is loaded into this slot.
+        auto stage = [&](int kt, int slot, int flip, auto MORE, auto LOAD, auto WAIT) {
+            constexpr bool more = decltype(MORE)::value, loads = decltype(LOAD)::value;
+            const int next = slot + 1 == S ? 0 : slot + 1;
+            sw = read_w_scale(slot);
+#pragma unroll
+            for (int i = 0; i < FI; ++i) sx[i] = read_scale(slot, i);
+#pragma unroll
+            for (int i = 0; i < FI; ++i) {
+                if (i + 1 < FI) fa[(i + 1) & 1] = read_a(slot, i + 1);
+                if (i + 1 == FI && more) {
+                    wait_loads<decltype(WAIT)::value>();
+                    group_barrier();
+                }
+                const float s = sx[i] * sw;
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) {
+                    const f32x4 v = mfma_fp8(fb[j], fa[i & 1]);
+                    if (i + 1 == FI && more) fb[j] = read_b(next, j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], s, acc[i][j][e]);
+                }
+                if (i + 1 == FI) {
+                    if constexpr (more) fa[0] = read_a(next, 0);
+                    if constexpr (loads) {
+#pragma unroll
+                        for (int d = 0; d < DPW; ++d) load(d, kt + S, slot);
+                    }
+                }
+            }
+        };
+        using yes = std::true_type;
+        using no = std::false_type;
+        int kt = 0, slot = 0;
+        for (; kt + S < KT; ++kt) {
+            stage(kt, slot, 0, yes{}, yes{}, std::integral_constant<int, (S - 2) * DPW>{});
+            slot = slot + 1 == S ? 0 : slot + 1;
+        }
+        for (; kt + 1 < KT; ++kt) {
+            stage(kt, slot, 0, yes{}, no{}, std::integral_constant<int, 0>{});
+            slot = slot + 1 == S ? 0 : slot + 1;
+        }
+        stage(kt, slot, 0, no{}, no{}, std::integral_constant<int, 0>{});
+
+        // A lane holds row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 block.
+        if constexpr (!STAGED) {
+            float* out = PART ? p.part + (int64_t)blockIdx.y * p.m * p.n : (float*)p.y;
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) {
+                    const int row = m0 + (wm * FI + i) * 16 + (lane & 15);
+                    const int col = n0 + (wn * FJ + j) * 16 + (lane >> 4) * 4;
+                    if (row < p.m) keep_n<4>(out + (int64_t)row * p.n, col, p.n, (const float*)&acc[i][j]);
+                }
+        } else {
+            group_barrier();
+            constexpr int PITCH = FJ * 32, CPR = FJ * 2, RPI = 64 / CPR;
+            static_assert(64 % CPR == 0 && (FI * 16) % RPI == 0, "staging layout");
+            COC_LDS uint8_t* stg = (COC_LDS uint8_t*)sm + wave * (FI * 16 * PITCH);
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) {
+                    const int row = i * 16 + (lane & 15), ch = j * 2 + (lane >> 5);
+                    *(COC_LDS u32x2*)(stg + row * PITCH + ((ch ^ (row & (CPR - 1))) << 4) + ((lane >> 4) & 1) * 8) =
+                        u32x2{round2<T>(acc[i][j][0], acc[i][j][1]), round2<T>(acc[i][j][2], acc[i][j][3])};
+                }
+#pragma unroll
+            for (int t = 0; t < FI * 16 / RPI; ++t) {
+                const int row = t * RPI + lane / CPR, ch = lane % CPR;
+                const u32x4 v = *(const COC_LDS u32x4*)(stg + row * PITCH + ((ch ^ (row & (CPR - 1))) << 4));
+                const int r = m0 + wm * FI * 16 + row, col = n0 + wn * FJ * 16 + ch * 8;
+                Packed<T> o;
+                __builtin_memcpy(o.w, &v, 16);
+                if (r < p.m && col < p.n) keep_raw((T*)p.y + (int64_t)r * p.n, col, p.n, o);
+            }
+        }
+    }
+
+    // (stored normally: a product's result is read next)
+    static __device__ __forceinline__ void keep_raw(T* row, int c, int n, const Packed<T>& o) {
+        if (c + kVec<T> <= n)
+            __builtin_memcpy(row + c, o.w, 16);
+        else
+            store_raw(row, c, n, o);
+    }
+};
+
+template <class Tile, int THREADS, int PER_EU>
+__global__ __launch_bounds__(THREADS, PER_EU) void fp8_tile(Fp8Params p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[Tile::LDS];
+    Tile::run(p, sm);
+}
+
+// Adds the splits' sums in order.  Four columns a thread.
+template <class T>
+__global__ __launch_bounds__(256) void fp8_join(const float* part, T* y, int64_t m, int n, int splits) {
+    const int per_row = (n + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= m * per_row) return;
+    const int64_t row = i / per_row;
+    const int col = (int)(i - row * per_row) * 4;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) {
+        float t[4];
+        load_vec(part + (s * m + row) * n, col, n, t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += t[e];
+    }
+    keep_n<4>(y + row * n, col, n, v);
+}
+
+constexpr int64_t kCus = 256;   // of an MI355X
+
+struct Choice {
+    int tile;   // 0: 256 x 256, 1: 128 x 128, 2: the same split, 3 .. 5: 64, 32, 16 rows by 128, split
+    int stages, splits;
+};
+
+// As for the 16-bit products: the largest tile that still gives most CUs one, then smaller
+// ones, then the k range split too; few rows take a tile of as few.
+Choice choose(int64_t m, int64_t n, int64_t k) {
+    const int64_t stages = ceil_div(k, kScaleBlock);
+    if (m > 64 && ceil_div(m, 256) * ceil_div(n, 256) >= kCus * 3 / 4) return {0, (int)stages, 1};
+    const int64_t rows = m > 64 ? 128 : m > 32 ? 64 : m > 16 ? 32 : 16;
+    const int64_t tiles = ceil_div(m, rows) * ceil_div(n, 128);
+    int64_t splits = 2 * kCus / tiles;
+    if (splits > stages / 4) splits = stages / 4;
+    if (splits < 1) splits = 1;
+    const int64_t each = ceil_div(stages, splits);
+    splits = ceil_div(stages, each);
+    if (rows == 128) return {splits > 1 ? 2 : 1, (int)each, (int)splits};
+    return {rows == 64 ? 3 : rows == 32 ? 4 : 5, (int)each, (int)splits};
+}
+
+size_t part_bytes(int64_t m, int64_t n, int64_t k) {
+    const Choice c = choose(m, n, k);
+    return c.tile >= 2 ? (size_t)(c.splits * m * n * 4) : 0;
+}
+
+template <class Tile, int THREADS, int PER_EU>
+void launch_tile(Fp8Params p, const Choice& c, hipStream_t stream) {
+    p.tiles_m = (int)ceil_div(p.m, Tile::BM);
+    p.tiles_n = (int)ceil_div(p.n, Tile::BN);
+    p.stages = c.stages;
+    fp8_tile<Tile, THREADS, PER_EU>
+        <<<dim3((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)c.splits), dim3(THREADS), 0, stream>>>(p);
+}
+
+coc_status check_product(int64_t m, int64_t n, int64_t k, coc_dtype dt) {
+    if (!dtype_valid(dt)) return fail(COC_ERR_DTYPE, "unknown dtype %d", (int)dt);
+    if (k < 0 || k % 16 != 0) return fail(COC_ERR_SHAPE, "k is a multiple of 16 (k=%lld)", (long long)k);
+    coc_status st = check_matrix(m, k, "x");
+    if (st == COC_OK) st = check_matrix(n, k, "w");
+    if (st == COC_OK) st = check_matrix(m, n, "y");
+    return st;
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void fp8_zeros(T* y, int64_t count) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < count) y[i] = (T)0.0f;
+}
+
+}  // namespace
+}  // namespace coc
+
+extern "C" {
+
+size_t coc_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (m <= 0 || n <= 0 || k <= 0 || coc::check_product(m, n, k, COC_F32) != COC_OK) return 0;
+    return coc::part_bytes(m, n, k);
+}
+
+coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
+                          int64_t m, int64_t n, int64_t k, coc_dtype dt, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+    using namespace coc;
+    clear_error();
+    coc_status st = check_product(m, n, k, dt);
+    if (st != COC_OK) return st;
+    if (m == 0 || n == 0) return COC_OK;
+    const size_t need = k > 0 ? part_bytes(m, n, k) : 0;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(COC_ERR_WORKSPACE, "matmul_fp8 needs %zu workspace bytes (got %zu)", need,
+                    ws ? ws_bytes : (size_t)0);
+    const int32_t es = (int32_t)elem_size(dt);
+    const int64_t blocks = ceil_div(k, kScaleBlock);
+    const Arg args[] = {{x, m * k, 16, false, "x"},
+                        {x_scales, blocks * m * 4, 4, false, "x_scales"},
+                        {w, n * k, 16, false, "w"},
+                        {w_scales, ceil_div(n, kScaleBlock) * blocks * 4, 4, false, "w_scales"},
+                        {y, m * n * es, es, true, "y"},
+                        {ws, (int64_t)need, 16, true, "ws"}};
+    st = check_args(args, 6);
+    if (st != COC_OK) return st;
+    auto by_out = [&](auto&& f) {
+        if (dt == COC_F32)
+            f(float());
+        else if (dt == COC_F16)
+            f(f16_t());
+        else
+            f(bf16_t());
+    };
+    if (k == 0) {
+        by_out([&](auto t) {
+            using T = decltype(t);
+            fp8_zeros<T><<<dim3((uint32_t)ceil_div(m * n, 256)), dim3(256), 0, stream>>>((T*)y, m * n);
+        });
+        return launched("matmul_fp8");
+    }
+    Fp8Params p{};
+    p.x = (const uint8_t*)x;
+    p.w = (const uint8_t*)w;
+    p.xs = x_scales;
+    p.ws = w_scales;
+    p.y = y;
+    p.part = (float*)ws;
+    p.m = (int)m;
+    p.n = (int)n;
+    p.k = (int)k;
+    p.blocks = (int)blocks;
+    const Choice c = choose(m, n, k);
+    switch (c.tile) {
+        case 0: by_out([&](auto t) { launch_tile<Fp8Tile<decltype(t), 8, 4, 2, 4, 2, false>, 512, 2>(p, c, stream); }); break;
+        case 1: by_out([&](auto t) { launch_tile<Fp8Tile<decltype(t), 4, 4, 2, 2, 2, false>, 256, 2>(p, c, stream); }); break;
+        case 2: launch_tile<Fp8Tile<float, 4, 4, 2, 2, 2, true>, 256, 2>(p, c, stream); break;
+        case 3: launch_tile<Fp8Tile<float, 4, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
+        case 4: launch_tile<Fp8Tile<float, 2, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
+        default: launch_tile<Fp8Tile<float, 1, 2, 1, 4, 4, true>, 256, 2>(p, c, stream); break;
+    }
+    st = launched("matmul_fp8");
+    if (st != COC_OK || c.tile < 2) return st;
+    by_out([&](auto t) {
+        using T = decltype(t);
+        fp8_join<T><<<dim3((uint32_t)ceil_div(m * ceil_div(n, 4), 256)), dim3(256), 0, stream>>>((const float*)ws, (T*)y,
+                                                                                                 m, (int)n, c.splits);
+    });
+    return launched("matmul_fp8 join");
+}
+
+}  // extern "C"
