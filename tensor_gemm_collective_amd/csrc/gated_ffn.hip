@@ -95,7 +95,7 @@ void launch_tile(MmParams p, const Choice& c, hipStream_t stream) {
     p.tiles_m = (int)ceil_div(p.m, Tile::BM);
     p.tiles_n = (int)ceil_div(p.n, Tile::OUT);
     p.stages = c.stages;
-    mm_tile<Tile><<<dim3((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)c.splits), dim3(256), 0, stream>>>(p);
+    mm_tile<Tile><<<dim3((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)c.splits), dim3(Tile::NW * 64), 0, stream>>>(p);
 }
 
 // C = A B of these sizes by the chosen tile, joined where it is split.
@@ -103,7 +103,7 @@ template <class T, bool TA, bool TB, bool GATED>
 coc_status product(MmParams p, hipStream_t stream) {
     const Choice c = choose(p.m, p.n, p.k, GATED, TA);
     switch (c.tile) {
-        case 0: launch_tile<MmTile<T, TA, TB, 8, 8, 2, 2, 2, GATED, false>>(p, c, stream); break;
+        case 0: launch_tile<MmTile<T, TA, TB, 8, 4, 2, 4, 2, GATED, false>>(p, c, stream); break;
         case 1: launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, false>>(p, c, stream); break;
         case 2: launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, true>>(p, c, stream); break;
         case 3: launch_tile<MmTile<T, TA, TB, 4, 2, 1, 4, 3, GATED, true>>(p, c, stream); break;

@@ -105,10 +105,11 @@ struct Operand {
     static_assert(!TRANS || CHUNKS == 8 || CHUNKS == 16 || CHUNKS == 32, "k rows of 64, 128 or 256 elements");
 
     uint32_t off[PER_WAVE];   // from the stage's base, bytes
-    int at[PER_WAVE];         // its k within the stage
+    int q0;                   // this lane's chunk of the first load
     const uint8_t* base;
     int64_t step;             // bytes from stage to stage
-    uint32_t lds;             // this wave's first load's place in slot 0
+    uint32_t lds;             // its place in slot 0; NEXT later for each further load
+    static constexpr uint32_t NEXT = INS >= NW ? NW * 1024 : 1024;
 
     // first(local row or column) -> the global one to read; ld: elements from row to row
     template <class F>
@@ -116,30 +117,35 @@ struct Operand {
                                          F&& first) {
         step = TRANS ? STEP * ld * ES : 128;
         base = (const uint8_t*)p + stage0 * step;
+        q0 = wave % INS * 64 + lane;   // load i of the waves together: neighbouring rows
 #pragma unroll
         for (int i = 0; i < PER_WAVE; ++i) {
-            const int q = ((wave * PER_WAVE + i) % INS) * 64 + lane;
+            const int q = q0 + i * NW * 64;
             if constexpr (TRANS) {
                 const int k = q / CHUNKS, c = (q % CHUNKS) ^ k_swizzle<CHUNKS>(k);
-                at[i] = k;
                 off[i] = (uint32_t)k * (uint32_t)ld * 2 + (uint32_t)first(c * 8) * 2;
             } else {
                 const int r = q >> 3, c = (q & 7) ^ row_swizzle(r);
-                at[i] = c * (16 / ES);
                 off[i] = (uint32_t)((int64_t)first(r) * ld * ES) + (uint32_t)c * 16;
             }
         }
-        lds = lds0 + ((wave * PER_WAVE) % INS) * 1024;
+        lds = lds0 + wave % INS * 1024;
+    }
+    // the k of load i's chunk within its stage
+    __device__ __forceinline__ int at(int i) const {
+        const int q = q0 + i * NW * 64;
+        return TRANS ? q / CHUNKS : ((q & 7) ^ row_swizzle(q >> 3)) * (16 / ES);
     }
     // load i of stage s (counted from stage0) into the slot `slot_bytes` on; left: how
-    // many k the stage has
+    // many k the stage has (WHOLE: all)
+    template <bool WHOLE>
     __device__ __forceinline__ void load(int i, int s, uint32_t slot_bytes, int left) const {
         const uint8_t* b = base + s * step;
-        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + slot_bytes + i * 1024);
-        if (left >= STEP)
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + slot_bytes + i * NEXT);
+        if (WHOLE || left >= STEP)
             load_lds(off[i], b, to);
         else
-            load_lds_at(at[i] < left ? (const void*)(b + off[i]) : (const void*)&g_zeros, to);
+            load_lds_at(at(i) < left ? (const void*)(b + off[i]) : (const void*)&g_zeros, to);
     }
 };
 

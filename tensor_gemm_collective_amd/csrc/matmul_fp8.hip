@@ -1,6 +1,8 @@
 // Matrix product of 8-bit floating-point operands with a scale for each block of 128:
 //   y[i][j] = sum over blocks b of  xs[b][i] ws[j / 128][b]  sum over k in b of  x[i][k] w[j][k].
 // x's scales cover 128 of a row, w's 128 x 128.
+#include <algorithm>
+
 #include "fp8.h"
 #include "lds_tile.h"
 
@@ -8,6 +10,7 @@ namespace coc {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 struct Fp8Params {
     const uint8_t *x, *w;
@@ -18,9 +21,41 @@ struct Fp8Params {
     int tiles_m, tiles_n, stages;   // stages: blocks of one split
 };
 
-// 128 k of 16 x 16 outputs.
-__device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+// A lane's 32 values of a fragment as the MFMAs take them: the bytes, or (WIDE) binary16,
+// which holds every e4m3 value.
+template <bool WIDE>
+struct Values {
+    i32x8 v;
+    __device__ __forceinline__ void set(i32x8 bytes) { v = bytes; }
+};
+template <>
+struct Values<true> {
+    u32x4 v[4];
+    __device__ __forceinline__ void set(i32x8 bytes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i >> 1][(i & 1) * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(bytes[i], 1.0f, false));
+            v[i >> 1][(i & 1) * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(bytes[i], 1.0f, true));
+        }
+    }
+};
+
+// 128 k of 16 x 16 outputs.  The 8-bit MFMA adds each lane's products in groups of eight
+// neighbouring k, in which bits below 2^-13 of the largest product's power of two are
+// dropped (measured: a product 2^-13 of another is kept, one of 2^-14 is not, and beyond
+// the group 2^-23 is), and then the groups in binary32: about 2e-5 of the result, a tenth
+// of a rounding to binary16.  Results in binary32 are formed by 16-bit MFMAs, which hold
+// every product whole, at half the rate.
+__device__ __forceinline__ f32x4 mfma_block(const Values<false>& a, const Values<false>& b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_block(const Values<true>& a, const Values<true>& b) {
+    f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v[q]), __builtin_bit_cast(f16x8, b.v[q]), c,
+                                                   0, 0, 0);
+    return c;
 }
 
 // One BM x BN tile.  A stage is one block of 128 k, so each MFMA gives a whole block's sum,
@@ -29,7 +64,7 @@ __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
 // operand: a lane then holds one row of x in each 16 x 16 block and needs one scale for
 // it.  A lane's 32 k of a fragment are chunks g and g + 4 of a row (g: its 16-lane group)
 // for both operands; the order of k within a block is free.
-template <class T, int FI, int FJ, int WM, int WN, int S, bool PART>
+template <class T, bool WIDE, int FI, int FJ, int WM, int WN, int S, bool PART>
 struct Fp8Tile {
     static constexpr int NW = WM * WN, BM = WM * FI * 16, BN = WN * FJ * 16, NB = BN / kScaleBlock;
     using A = Operand<BM, false, NW, 1>;
@@ -39,6 +74,10 @@ struct Fp8Tile {
     static constexpr int SLOT = A::BYTES + B::BYTES + SCALES;
     static constexpr int LDS = S * SLOT;
     static constexpr int DPW = A::PER_WAVE + B::PER_WAVE + 1;
+    // whether a stage's loads go in two parts (see stage): with as many waves as row
+    // blocks, load i of the rows is the lower half of the waves' blocks for even i
+    static constexpr bool HALVES = FI == NW;
+    static constexpr int EARLY = HALVES ? B::PER_WAVE + A::PER_WAVE / 2 : 0;
     static constexpr bool STAGED = !PART && sizeof(T) == 2;   // rows go out through the LDS
     static_assert(BN % kScaleBlock == 0 && kScaleBlock % (FJ * 16) == 0, "a wave's columns share a scale");
     static_assert(XW < NW, "a wave for w's scales");
@@ -66,12 +105,16 @@ struct Fp8Tile {
         const int64_t scale_step = of_x ? (int64_t)p.m * 4 : 4;
         const uint8_t* scale_base = (const uint8_t*)(of_x ? p.xs : p.ws) + stage0 * scale_step;
         const uint32_t scale_lds = lds0 + A::BYTES + B::BYTES + (of_x ? wave : XW) * 256;
-        auto load = [&](int d, int s, int slot) {
+        auto load = [&](int d, int s, int slot, auto WHOLE) {
+            constexpr bool whole = decltype(WHOLE)::value;
             const int left = p.k - (stage0 + s) * kScaleBlock;
-            if (d < A::PER_WAVE)
-                a.load(d, s, slot * SLOT, left);
-            else if (d < A::PER_WAVE + B::PER_WAVE)
-                b.load(d - A::PER_WAVE, s, slot * SLOT, left);
+            // the columns, the even loads of the rows, the odd ones, the scales
+            constexpr int NB_ = B::PER_WAVE, NE = HALVES ? A::PER_WAVE / 2 : 0;
+            if (d < NB_)
+                b.template load<whole>(d, s, slot * SLOT, left);
+            else if (d < NB_ + A::PER_WAVE)
+                a.template load<whole>(!HALVES ? d - NB_ : d < NB_ + NE ? 2 * (d - NB_) : 2 * (d - NB_ - NE) + 1, s,
+                                       slot * SLOT, left);
             else
                 load_lds4(scale_off, scale_base + s * scale_step,
                           __builtin_amdgcn_readfirstlane(scale_lds + slot * SLOT));
@@ -87,8 +130,10 @@ struct Fp8Tile {
         const COC_LDS uint8_t* lds = (const COC_LDS uint8_t*)sm;
         auto fragment = [&](int at0, int at1) {
             const u32x4 lo = *(const COC_LDS u32x4*)(lds + at0), hi = *(const COC_LDS u32x4*)(lds + at1);
-            return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4,
-                                           5, 6, 7);
+            Values<WIDE> f;
+            f.set(__builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5,
+                                          6, 7));
+            return f;
         };
         auto read_a = [&](int slot, int i) {
             return fragment(slot * SLOT + pa[0] + i * 2048, slot * SLOT + pa[1] + i * 2048);
@@ -112,14 +157,13 @@ struct Fp8Tile {
 
         for (int s = 0; s < S && s < KT; ++s)
 #pragma unroll
-            for (int d = 0; d < DPW; ++d) load(d, s, s);
+            for (int d = 0; d < DPW; ++d) load(d, s, s, std::false_type());
         if (KT >= S)
             wait_loads<(S - 1) * DPW>();
         else
             wait_loads<0>();
         group_barrier();
-        i32x8 fa[2], fb[FJ];
-        float sx[FI], sw;
+        Values<WIDE> fa[2], fb[FJ];
 #pragma unroll
         for (int j = 0; j < FJ; ++j) fb[j] = read_b(0, j);
         fa[0] = read_a(0, 0);
@@ -127,49 +171,75 @@ struct Fp8Tile {
         // One stage.  The next row block's fragment is read under this one's MFMAs; before
         // the last row block the workgroup meets (every wave has read this slot, and the
         // next stage has arrived), and under its MFMAs the next stage's first fragments are
-        // read and stage kt + S is loaded into this slot.
-        auto stage = [&](int kt, int slot, int flip, auto MORE, auto LOAD, auto WAIT) {
+        // read and stage kt + S is loaded into this slot.  HALVES: the workgroup also meets
+        // half way, when the columns and the lower row blocks have been read, and loads
+        // their places then: half a stage more to arrive in, and loads that do not come in
+        // one burst.
+        auto stage = [&](int kt, int slot, auto MORE, auto LOAD, auto WHOLE, auto WAIT) {
             constexpr bool more = decltype(MORE)::value, loads = decltype(LOAD)::value;
+            constexpr int N = FI * FJ, HALF = N / 2, LAST = N - FJ;
             const int next = slot + 1 == S ? 0 : slot + 1;
-            sw = read_w_scale(slot);
+            f32x4 sum[3];     // of the last three MFMAs
+            float sx[2];
+            const float sw = read_w_scale(slot);
+            sx[0] = read_scale(slot, 0);
+            auto add = [&](int t) {
+                const int i = t / FJ, j = t % FJ;
+                const float s = sx[i & 1];
 #pragma unroll
-            for (int i = 0; i < FI; ++i) sx[i] = read_scale(slot, i);
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sum[t % 3][e], s, acc[i][j][e]);
+                asm volatile("" : "+v"(acc[i][j]));   // here, not at the end of the stage
+            };
 #pragma unroll
-            for (int i = 0; i < FI; ++i) {
-                if (i + 1 < FI) fa[(i + 1) & 1] = read_a(slot, i + 1);
-                if (i + 1 == FI && more) {
+            for (int t = 0; t < N; ++t) {
+                const int i = t / FJ, j = t % FJ;
+                if (HALVES && loads && t == HALF) {
+                    wait_loads<63>();
+                    group_barrier();
+                }
+                if (more && t == LAST) {
                     wait_loads<decltype(WAIT)::value>();
                     group_barrier();
                 }
-                const float s = sx[i] * sw;
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) {
-                    const f32x4 v = mfma_fp8(fb[j], fa[i & 1]);
-                    if (i + 1 == FI && more) fb[j] = read_b(next, j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], s, acc[i][j][e]);
-                }
-                if (i + 1 == FI) {
-                    if constexpr (more) fa[0] = read_a(next, 0);
-                    if constexpr (loads) {
-#pragma unroll
-                        for (int d = 0; d < DPW; ++d) load(d, kt + S, slot);
+                sum[t % 3] = mfma_block(fb[j], fa[i & 1]);
+                if (t >= 2) add(t - 2);
+                if (t % FJ == (FJ > 1 ? 1 : 0)) sx[i & 1] *= sw;   // (the row block's sums are added from here on)
+                if (i + 1 < FI) {
+                    if (j == 0) fa[(i + 1) & 1] = read_a(slot, i + 1);
+                    if (j + 1 == FJ) sx[(i + 1) & 1] = read_scale(slot, i + 1);
+                } else {
+                    if constexpr (more) {
+                        fb[j] = read_b(next, j);
+                        if (j + 1 == FJ) fa[0] = read_a(next, 0);
                     }
                 }
+                if constexpr (loads) {
+#pragma unroll
+                    for (int d = 0; d < DPW; ++d)
+                        if (d < EARLY ? d * (LAST - HALF) / (EARLY > 0 ? EARLY : 1) + HALF == t
+                                      : (d - EARLY) * FJ / (DPW - EARLY) + LAST == t)
+                            load(d, kt + S, slot, WHOLE);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            add(N - 2);
+            add(N - 1);
         };
         using yes = std::true_type;
         using no = std::false_type;
         int kt = 0, slot = 0;
-        for (; kt + S < KT; ++kt) {
-            stage(kt, slot, 0, yes{}, yes{}, std::integral_constant<int, (S - 2) * DPW>{});
-            slot = slot + 1 == S ? 0 : slot + 1;
+        using all = std::integral_constant<int, (S - 2) * DPW + EARLY>;
+        using none = std::integral_constant<int, 0>;
+        auto step = [&] { slot = slot + 1 == S ? 0 : slot + 1; };
+        // the last stage alone may be short of k
+        for (; kt + S + 1 < KT; ++kt, step()) stage(kt, slot, yes(), yes(), yes(), all());
+        if (kt + S < KT) {
+            stage(kt, slot, yes(), yes(), no(), all());
+            ++kt;
+            step();
         }
-        for (; kt + 1 < KT; ++kt) {
-            stage(kt, slot, 0, yes{}, no{}, std::integral_constant<int, 0>{});
-            slot = slot + 1 == S ? 0 : slot + 1;
-        }
-        stage(kt, slot, 0, no{}, no{}, std::integral_constant<int, 0>{});
+        for (; kt + 1 < KT; ++kt, step()) stage(kt, slot, yes(), no(), no(), none());
+        stage(kt, slot, no(), no(), no(), none());
 
         // A lane holds row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 block.
         if constexpr (!STAGED) {
@@ -248,10 +318,11 @@ struct Choice {
 };
 
 // As for the 16-bit products: the largest tile that still gives most CUs one, then smaller
-// ones, then the k range split too; few rows take a tile of as few.
-Choice choose(int64_t m, int64_t n, int64_t k) {
+// ones, then the k range split too; few rows take a tile of as few.  wide: binary32
+// results, whose 16-bit fragments do not fit the largest tile's registers.
+Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
     const int64_t stages = ceil_div(k, kScaleBlock);
-    if (m > 64 && ceil_div(m, 256) * ceil_div(n, 256) >= kCus * 3 / 4) return {0, (int)stages, 1};
+    if (!wide && m > 64 && ceil_div(m, 256) * ceil_div(n, 256) >= kCus * 3 / 4) return {0, (int)stages, 1};
     const int64_t rows = m > 64 ? 128 : m > 32 ? 64 : m > 16 ? 32 : 16;
     const int64_t tiles = ceil_div(m, rows) * ceil_div(n, 128);
     int64_t splits = 2 * kCus / tiles;
@@ -263,8 +334,8 @@ Choice choose(int64_t m, int64_t n, int64_t k) {
     return {rows == 64 ? 3 : rows == 32 ? 4 : 5, (int)each, (int)splits};
 }
 
-size_t part_bytes(int64_t m, int64_t n, int64_t k) {
-    const Choice c = choose(m, n, k);
+size_t part_bytes(int64_t m, int64_t n, int64_t k, bool wide) {
+    const Choice c = choose(m, n, k, wide);
     return c.tile >= 2 ? (size_t)(c.splits * m * n * 4) : 0;
 }
 
@@ -299,7 +370,7 @@ extern "C" {
 
 size_t coc_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
     if (m <= 0 || n <= 0 || k <= 0 || coc::check_product(m, n, k, COC_F32) != COC_OK) return 0;
-    return coc::part_bytes(m, n, k);
+    return std::max(coc::part_bytes(m, n, k, false), coc::part_bytes(m, n, k, true));
 }
 
 coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
@@ -310,7 +381,7 @@ coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, c
     coc_status st = check_product(m, n, k, dt);
     if (st != COC_OK) return st;
     if (m == 0 || n == 0) return COC_OK;
-    const size_t need = k > 0 ? part_bytes(m, n, k) : 0;
+    const size_t need = coc_matmul_fp8_workspace_bytes(m, n, k);
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(COC_ERR_WORKSPACE, "matmul_fp8 needs %zu workspace bytes (got %zu)", need,
                     ws ? ws_bytes : (size_t)0);
@@ -350,15 +421,27 @@ coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, c
     p.n = (int)n;
     p.k = (int)k;
     p.blocks = (int)blocks;
-    const Choice c = choose(m, n, k);
-    switch (c.tile) {
-        case 0: by_out([&](auto t) { launch_tile<Fp8Tile<decltype(t), 8, 4, 2, 4, 2, false>, 512, 2>(p, c, stream); }); break;
-        case 1: by_out([&](auto t) { launch_tile<Fp8Tile<decltype(t), 4, 4, 2, 2, 2, false>, 256, 2>(p, c, stream); }); break;
-        case 2: launch_tile<Fp8Tile<float, 4, 4, 2, 2, 2, true>, 256, 2>(p, c, stream); break;
-        case 3: launch_tile<Fp8Tile<float, 4, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
-        case 4: launch_tile<Fp8Tile<float, 2, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
-        default: launch_tile<Fp8Tile<float, 1, 2, 1, 4, 4, true>, 256, 2>(p, c, stream); break;
-    }
+    const Choice c = choose(m, n, k, dt == COC_F32);
+    auto go = [&](auto t, auto wide) {
+        using T = decltype(t);
+        constexpr bool WIDE = decltype(wide)::value;
+        switch (c.tile) {
+            case 0:
+                if constexpr (!WIDE) launch_tile<Fp8Tile<T, WIDE, 8, 4, 2, 4, 2, false>, 512, 2>(p, c, stream);
+                break;
+            case 1: launch_tile<Fp8Tile<T, WIDE, 4, 4, 2, 2, 2, false>, 256, 2>(p, c, stream); break;
+            case 2: launch_tile<Fp8Tile<float, WIDE, 4, 4, 2, 2, 2, true>, 256, 2>(p, c, stream); break;
+            case 3: launch_tile<Fp8Tile<float, WIDE, 4, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
+            case 4: launch_tile<Fp8Tile<float, WIDE, 2, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
+            default: launch_tile<Fp8Tile<float, WIDE, 1, 2, 1, 4, 4, true>, 256, 2>(p, c, stream); break;
+        }
+    };
+    if (dt == COC_F32)
+        go(float(), std::true_type());
+    else if (dt == COC_F16)
+        go(f16_t(), std::false_type());
+    else
+        go(bf16_t(), std::false_type());
     st = launched("matmul_fp8");
     if (st != COC_OK || c.tile < 2) return st;
     by_out([&](auto t) {

@@ -1,6 +1,6 @@
 // The 16-bit MFMA tile of the gated feed-forward block's products.
 //
-// C (m x n) = A B over k in binary32, four waves a workgroup, each a block of FI x FJ
+// C (m x n) = A B over k in binary32, WM x WN waves a workgroup, each a block of FI x FJ
 // v_mfma_f32_16x16x32 outputs.  k runs in stages of 64 through S LDS slots that
 // direct-to-LDS loads fill ahead of the waves (lds_tile.h).  Rows and columns past m and
 // n are read clamped and not stored.
@@ -120,12 +120,13 @@ struct MmTile {
         Fragments<BN, !TB> fb;
         fa.init(wm * FI * 16, lane);
         fb.init(wn * FJ * 16, lane);
-        auto load = [&](int d, int s, int slot) {
+        auto load = [&](int d, int s, int slot, auto WHOLE) {
+            constexpr bool whole = decltype(WHOLE)::value;
             const int left = p.k - k0 - s * 64;
             if (d < A::PER_WAVE)
-                a.load(d, s, slot * SLOT, left);
+                a.template load<whole>(d, s, slot * SLOT, left);
             else
-                b.load(d - A::PER_WAVE, s, slot * SLOT, left);
+                b.template load<whole>(d - A::PER_WAVE, s, slot * SLOT, left);
         };
         u32x4 af[2][FI], bf[2][FJ];
         // read r of a k step's: the first row block, the columns, the other row blocks
@@ -147,7 +148,7 @@ struct MmTile {
 
         for (int s = 0; s < S && s < KT; ++s)
 #pragma unroll
-            for (int d = 0; d < DPW; ++d) load(d, s, s);
+            for (int d = 0; d < DPW; ++d) load(d, s, s, std::false_type());
         if (KT >= S)
             wait_loads<(S - 1) * DPW>();
         else
@@ -160,7 +161,7 @@ struct MmTile {
         // MFMAs; a quarter into the second the workgroup meets (every wave has read
         // this slot, and the next stage has arrived), then the next stage's first
         // fragments are read and stage kt + S is loaded into this slot.
-        auto stage = [&](int kt, int slot, auto MORE, auto LOAD, auto WAIT) {
+        auto stage = [&](int kt, int slot, auto MORE, auto LOAD, auto WHOLE, auto WAIT) {
             constexpr bool more = decltype(MORE)::value, loads = decltype(LOAD)::value;
             const int next = slot + 1 == S ? 0 : slot + 1;
             __builtin_amdgcn_sched_barrier(0);
@@ -194,7 +195,7 @@ struct MmTile {
                 if constexpr (loads) {
 #pragma unroll
                     for (int d = 0; d < DPW; ++d)
-                        if (d * LEFT / DPW == g) load(d, kt + S, slot);
+                        if (d * LEFT / DPW == g) load(d, kt + S, slot, WHOLE);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -202,16 +203,19 @@ struct MmTile {
         using yes = std::true_type;
         using no = std::false_type;
         int kt = 0, slot = 0;
-        // at stage kt's barrier the stages kt + 1 .. kt + S - 1 are in flight
-        for (; kt + S < KT; ++kt) {
-            stage(kt, slot, yes{}, yes{}, std::integral_constant<int, (S - 2) * DPW>{});
-            slot = slot + 1 == S ? 0 : slot + 1;
+        using all = std::integral_constant<int, (S - 2) * DPW>;
+        using none = std::integral_constant<int, 0>;
+        auto step = [&] { slot = slot + 1 == S ? 0 : slot + 1; };
+        // at stage kt's barrier the stages kt + 1 .. kt + S - 1 are in flight; the last
+        // stage alone may be short of k
+        for (; kt + S + 1 < KT; ++kt, step()) stage(kt, slot, yes(), yes(), yes(), all());
+        if (kt + S < KT) {
+            stage(kt, slot, yes(), yes(), no(), all());
+            ++kt;
+            step();
         }
-        for (; kt + 1 < KT; ++kt) {
-            stage(kt, slot, yes{}, no{}, std::integral_constant<int, 0>{});
-            slot = slot + 1 == S ? 0 : slot + 1;
-        }
-        stage(kt, slot, no{}, no{}, std::integral_constant<int, 0>{});
+        for (; kt + 1 < KT; ++kt, step()) stage(kt, slot, yes(), no(), no(), none());
+        stage(kt, slot, no(), no(), no(), none());
 
         // A lane holds row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 block.
         if constexpr (PART) {
@@ -280,13 +284,12 @@ struct MmTile {
     }
 };
 
-// Workgroups a CU holds at once: by the LDS, and one where a wave's blocks fill its
-// registers.
+// Waves of a SIMD: workgroups a CU holds by their LDS, times a workgroup's waves.
 template <class Tile>
-constexpr int kPerCu = Tile::LDS > 80 * 1024 ? 1 : 2;
+constexpr int kWavesSimd = (Tile::LDS > 80 * 1024 ? 1 : 2) * Tile::NW / 4;
 
 template <class Tile>
-__global__ __launch_bounds__(256, kPerCu<Tile>) void mm_tile(MmParams p) {
+__global__ __launch_bounds__(Tile::NW * 64, kWavesSimd<Tile>) void mm_tile(MmParams p) {
     __shared__ __attribute__((aligned(1024))) uint8_t sm[Tile::LDS];
     Tile::run(p, sm);
 }
