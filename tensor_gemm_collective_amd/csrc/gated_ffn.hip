@@ -6,48 +6,47 @@
 namespace coc {
 namespace {
 
-constexpr int64_t kCus = 256;   // of an MI355X
-
 // ------------------------------------------------------------------ joining split sums
 // Adds the splits' sums in order: h and gate_up (either may be NULL) of the gated
-// product, or the plain product's result.  Eight columns a thread.
-template <class T, bool GATED>
+// product, or the plain product's result.  Four columns a thread, U splits loaded together.
+template <class T, bool GATED, int U>
 __global__ __launch_bounds__(256) void mm_join(const float* part, T* c, T* gate_up, int64_t m, int n, int splits,
                                                int act) {
-    const int per_row = n / 8;
+    const int per_row = n / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= m * per_row) return;
     const int64_t row = i / per_row;
-    const int col = (int)(i - row * per_row) * 8;
+    const int col = (int)(i - row * per_row) * 4;
     const int64_t all = GATED ? 2 * n : n;
-    auto sum = [&](int64_t at, float* v) {
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        for (int s = 0; s < splits; ++s) {
-            const f32x4* p = (const f32x4*)(part + (s * m + row) * all + at);
-            const f32x4 lo = p[0], hi = p[1];
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+    for (int s0 = 0; s0 < splits; s0 += U) {
+        f32x4 g[U], w[U];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] += lo[e];
-                v[4 + e] += hi[e];
-            }
+        for (int k = 0; k < U; ++k) {   // past the last: the last again, not added
+            const float* p = part + (min(s0 + k, splits - 1) * m + row) * all + col;
+            g[k] = *(const f32x4*)p;
+            if (GATED) w[k] = *(const f32x4*)(p + n);
         }
-    };
-    float v[8];
-    sum(col, v);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s0 + k < splits) {
+                v += g[k];
+                if (GATED) u += w[k];
+            }
+    }
+    auto put = [&](T* at, f32x4 o) { *(u32x2*)at = u32x2{round2<T>(o[0], o[1]), round2<T>(o[2], o[3])}; };
     if constexpr (GATED) {
-        float u[8];
-        sum(n + col, u);
         if (gate_up) {
-            store_vec(gate_up + row * 2 * n, col, n, v);
-            store_vec(gate_up + row * 2 * n + n, col, n, u);
+            put(gate_up + row * 2 * n + col, v);
+            put(gate_up + row * 2 * n + n + col, u);
         }
         if (!c) return;
         by_act((coc_act)act, [&](auto a) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = act_value<decltype(a)::value>(v[e]) * u[e];
+            for (int e = 0; e < 4; ++e) v[e] = act_value<decltype(a)::value>(v[e]) * u[e];
         });
     }
-    store_vec(c + row * n, col, n, v);
+    put(c + row * n + col, v);
 }
 
 template <class T>
@@ -57,37 +56,34 @@ __global__ __launch_bounds__(256) void fill_zeros(T* p, int64_t vectors) {
 }
 
 // ------------------------------------------------------------------ which tile
-// A product's shape: m x n outputs (n: f of the gated product, whose tiles hold twice
-// as many columns of B), k long.
-struct Choice {
-    int tile;        // 0: 256 x 256, 1: 128 x 128, 2: the same split, 3 .. 5: 64, 32, 16 rows by 128, split
-    int stages;      // 64-k stages of one split
-    int splits;
+// The tiles, their stages of 64 k timed on products of 100 to 1500 rows.  The largest reads
+// its operands least often.  128 x 128 comes with four slots, one workgroup a CU, for
+// products of few tiles, and with two slots and two workgroups a CU.  Tiles of few rows are
+// a pass over the weights and always leave sums to join.
+enum { kTile256, kTile128Deep, kTile128, kTile64, kTile32, kTile16, kTiles };
+constexpr TileCost kCosts[kTiles] = {
+    {256, 256, 1, 1.35f, 1.50f, true, false}, {128, 128, 1, 0.55f, 0.55f, true, false},
+    {128, 128, 2, 0.84f, 0.94f, true, true},  {64, 128, 2, 0.38f, 0.80f, true, true},
+    {32, 128, 2, 0.40f, 0.60f, false, true},  {16, 128, 2, 0.36f, 0.50f, false, true},
 };
 
-// The largest tile that still gives most CUs one, since it reads its operands least
-// often; below that 128 x 128 tiles, two a CU, and where these are too few to go round
-// the k range is split as well.  Few rows take a tile of as few: their products are a
-// pass over the weights, in as many pieces as keep every CU loading.
+// m x n outputs (n: f of the gated product, whose tiles hold twice as many columns of B).
+// Up to 32 rows take a tile of as few and two workgroups a CU.
 Choice choose(int64_t m, int64_t n, int64_t k, bool gated, bool ta) {
     const int64_t cols = gated ? 2 * n : n, stages = ceil_div(k, 64);
-    const int64_t big = ceil_div(m, 256) * ceil_div(cols, 256);
-    if (m > 64 && big >= kCus * 3 / 4) return {0, (int)stages, 1};
-    const int64_t rows = m > 64 ? 128 : m > 32 || ta ? 64 : m > 16 ? 32 : 16;
-    const int64_t tiles = ceil_div(m, rows) * ceil_div(cols, 128);
-    // a split of at least four stages, and at most 2 workgroups a CU in all
-    int64_t splits = 2 * kCus / tiles;
-    if (splits > stages / 4) splits = stages / 4;
-    if (splits < 1) splits = 1;
-    const int64_t each = ceil_div(stages, splits);
-    splits = ceil_div(stages, each);
-    if (rows == 128) return {splits > 1 ? 2 : 1, (int)each, (int)splits};
-    return {rows == 64 ? 3 : rows == 32 ? 4 : 5, (int)each, (int)splits};
+    if (m > 32 || ta) {
+        constexpr TileCost large[] = {kCosts[0], kCosts[1], kCosts[2], kCosts[3]};
+        return pick(large, m, cols, stages);
+    }
+    constexpr TileCost few32[] = {kCosts[kTile32]}, few16[] = {kCosts[kTile16]};
+    Choice c = m > 16 ? pick(few32, m, cols, stages) : pick(few16, m, cols, stages);
+    c.tile = m > 16 ? kTile32 : kTile16;
+    return c;
 }
 
 size_t part_bytes(int64_t m, int64_t n, int64_t k, bool gated, bool ta = false) {
     const Choice c = choose(m, n, k, gated, ta);
-    return c.tile >= 2 ? (size_t)(c.splits * m * (gated ? 2 * n : n) * 4) : 0;
+    return c.split ? (size_t)(c.splits * m * (gated ? 2 * n : n) * 4) : 0;
 }
 
 template <class Tile>
@@ -103,11 +99,21 @@ template <class T, bool TA, bool TB, bool GATED>
 coc_status product(MmParams p, hipStream_t stream) {
     const Choice c = choose(p.m, p.n, p.k, GATED, TA);
     switch (c.tile) {
-        case 0: launch_tile<MmTile<T, TA, TB, 8, 4, 2, 4, 2, GATED, false>>(p, c, stream); break;
-        case 1: launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, false>>(p, c, stream); break;
-        case 2: launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, true>>(p, c, stream); break;
-        case 3: launch_tile<MmTile<T, TA, TB, 4, 2, 1, 4, 3, GATED, true>>(p, c, stream); break;
-        case 4:
+        case kTile256: launch_tile<MmTile<T, TA, TB, 8, 4, 2, 4, 2, GATED, false>>(p, c, stream); break;
+        case kTile128Deep: launch_tile<MmTile<T, TA, TB, 4, 2, 2, 4, 4, GATED, false>>(p, c, stream); break;
+        case kTile128:
+            if (c.split)
+                launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, true>>(p, c, stream);
+            else
+                launch_tile<MmTile<T, TA, TB, 4, 4, 2, 2, 2, GATED, false>>(p, c, stream);
+            break;
+        case kTile64:
+            if (c.split)
+                launch_tile<MmTile<T, TA, TB, 2, 2, 2, 4, 3, GATED, true>>(p, c, stream);
+            else
+                launch_tile<MmTile<T, TA, TB, 2, 2, 2, 4, 3, GATED, false>>(p, c, stream);
+            break;
+        case kTile32:
             if constexpr (!TA) launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, true>>(p, c, stream);
             break;
         default:
@@ -115,9 +121,12 @@ coc_status product(MmParams p, hipStream_t stream) {
             break;
     }
     coc_status st = launched("gated feed-forward product");
-    if (st != COC_OK || c.tile < 2) return st;
-    mm_join<T, GATED><<<dim3((uint32_t)ceil_div((int64_t)p.m * (p.n / 8), 256)), dim3(256), 0, stream>>>(
-        p.part, (T*)p.c, (T*)p.gate_up, p.m, p.n, c.splits, p.act);
+    if (st != COC_OK || !c.split) return st;
+    by_splits(c.splits, [&](auto u) {
+        mm_join<T, GATED, decltype(u)::value>
+            <<<dim3((uint32_t)ceil_div((int64_t)p.m * (p.n / 4), 256)), dim3(256), 0, stream>>>(
+                p.part, (T*)p.c, (T*)p.gate_up, p.m, p.n, c.splits, p.act);
+    });
     return launched("gated feed-forward join");
 }
 

@@ -149,5 +149,65 @@ struct Operand {
     }
 };
 
+// ------------------------------------------------------------------ which tile (host)
+constexpr int64_t kCus = 256;   // of an MI355X
+
+// A tile as measured: its rows and columns (of the operands), the workgroups a CU holds,
+// and the time of a stage in us while there is at most one workgroup a CU (`light`) and
+// while there are more (`full`).  Whether it may be split along k.
+struct TileCost {
+    int rows, cols, per_cu;
+    float light, full;
+    bool whole, split;   // offered unsplit, offered split
+};
+
+struct Choice {
+    int tile;     // index into the costs
+    int stages;   // of one split
+    int splits;   // 1: not split
+    bool split;   // leaves sums for a joining kernel
+};
+
+// The tile and split of the least estimated time for an m x n product of `stages` stages:
+// rounds of workgroups times a round's stages, and for a split the joining kernel (5 us of
+// launches, and its sums written and read at 6 TB/s).
+template <int N>
+inline Choice pick(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t stages) {
+    Choice best{0, (int)stages, 1, false};
+    float least = 1e30f;
+    for (int t = 0; t < N; ++t) {
+        const TileCost& c = costs[t];
+        const int64_t tiles = ceil_div(m, c.rows) * ceil_div(n, c.cols);
+        for (int64_t s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (s == 1 ? !(c.whole || c.split) : !c.split) continue;
+            const int64_t each = ceil_div(stages, s);
+            if (s > 1 && (each < 2 || ceil_div(stages, each) != s)) continue;
+            const bool join = s > 1 || !c.whole;
+            const int64_t groups = tiles * s;
+            float us = (float)ceil_div(groups, kCus * c.per_cu) * (float)each * (groups <= kCus ? c.light : c.full);
+            if (join) us += 5.0f + (float)(s * m * n) * (8.0f / 6e6f);
+            if (us < least) {
+                least = us;
+                best = {t, (int)each, (int)s, join};
+            }
+            if (groups > 4 * kCus * c.per_cu) break;
+        }
+    }
+    return best;
+}
+
+// f(how many splits' sums a joining kernel loads together).
+template <class F>
+void by_splits(int splits, F&& f) {
+    if (splits <= 2)
+        f(std::integral_constant<int, 2>());
+    else if (splits <= 4)
+        f(std::integral_constant<int, 4>());
+    else if (splits <= 8)
+        f(std::integral_constant<int, 8>());
+    else
+        f(std::integral_constant<int, 16>());
+}
+
 }  // namespace
 }  // namespace coc

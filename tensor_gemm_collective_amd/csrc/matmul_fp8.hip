@@ -292,8 +292,87 @@ __global__ __launch_bounds__(THREADS, PER_EU) void fp8_tile(Fp8Params p) {
     Tile::run(p, sm);
 }
 
-// Adds the splits' sums in order.  Four columns a thread.
-template <class T>
+// Up to 16 rows: a pass over the weights.  A workgroup takes 16 FJ rows of w and all of k,
+// its W waves every W-th block of 128 each, straight from memory into the MFMA's registers
+// (a load instruction reads 64 bytes of each of 16 rows, four blocks are loaded together);
+// the waves' sums are joined through the LDS, in order.
+template <class T, bool WIDE, int FJ, int W>
+__global__ __launch_bounds__(W * 64) void fp8_rows(Fp8Params p) {
+    constexpr int U = 4;
+    __shared__ float part[W][FJ][16][17];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16 * FJ, r = lane & 15, g = lane >> 4;
+    const uint8_t* pw[FJ];
+    const float* ws[FJ];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+        pw[j] = p.w + (int64_t)min(n0 + j * 16 + r, p.n - 1) * p.k + g * 16;
+        ws[j] = p.ws + (int64_t)(min(n0 + j * 16, p.n - 1) / kScaleBlock) * p.blocks;
+    }
+    const int mine = min(r, p.m - 1);
+    const uint8_t* px = p.x + (int64_t)mine * p.k + g * 16;
+    const float* xs = p.xs + mine;
+    f32x4 acc[FJ];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto take = [&](const uint8_t* at, int b, bool whole) {
+        // this lane's chunks g and g + 4 of block b
+        const int k = b * kScaleBlock + g * 16;
+        u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+        if (whole || k < p.k) lo = *(const u32x4*)(at + (int64_t)b * kScaleBlock);
+        if (whole || k + 64 < p.k) hi = *(const u32x4*)(at + (int64_t)b * kScaleBlock + 64);
+        return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6,
+                                       7);
+    };
+    auto blocks = [&](int b, auto COUNT, bool whole) {
+        constexpr int C = decltype(COUNT)::value;
+        i32x8 w[C][FJ], x[C];
+        float sw[C][FJ], sx[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = b + c * W;
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) w[c][j] = take(pw[j], at, whole);
+            x[c] = take(px, at, whole);
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) sw[c][j] = ws[j][at];
+            sx[c] = xs[(int64_t)at * p.m];
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            Values<WIDE> vx;
+            vx.set(x[c]);
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) {
+                Values<WIDE> vw;
+                vw.set(w[c][j]);
+                const f32x4 v = mfma_block(vw, vx);
+                const float s = sw[c][j] * sx[c];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(v[e], s, acc[j][e]);
+            }
+        }
+    };
+    const int whole = p.k / kScaleBlock;
+    int b = wave;
+    for (; b + (U - 1) * W < whole; b += U * W) blocks(b, std::integral_constant<int, U>(), true);
+    for (; b < p.blocks; b += W) blocks(b, std::integral_constant<int, 1>(), b < whole);
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[wave][j][r][g * 4 + e] = acc[j][e];
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t >= FJ * 256) return;
+    const int j = t >> 8, row = (t >> 4) & 15, col = t & 15, n = n0 + j * 16 + col;
+    float v = part[0][j][row][col];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += part[w][j][row][col];
+    if (row < p.m && n < p.n) ((T*)p.y)[(int64_t)row * p.n + n] = (T)v;
+}
+
+// Adds the splits' sums in order.  Four columns a thread, U splits loaded together.
+template <class T, int U>
 __global__ __launch_bounds__(256) void fp8_join(const float* part, T* y, int64_t m, int n, int splits) {
     const int per_row = (n + 3) / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -301,42 +380,56 @@ __global__ __launch_bounds__(256) void fp8_join(const float* part, T* y, int64_t
     const int64_t row = i / per_row;
     const int col = (int)(i - row * per_row) * 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) {
-        float t[4];
-        load_vec(part + (s * m + row) * n, col, n, t);
+    for (int s0 = 0; s0 < splits; s0 += U) {
+        float t[U][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += t[e];
+        for (int u = 0; u < U; ++u)   // past the last: the last again, not added
+            load_vec(part + (min(s0 + u, splits - 1) * m + row) * n, col, n, t[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += s0 + u < splits ? t[u][e] : 0.0f;
     }
     keep_n<4>(y + row * n, col, n, v);
 }
 
-constexpr int64_t kCus = 256;   // of an MI355X
-
-struct Choice {
-    int tile;   // 0: 256 x 256, 1: 128 x 128, 2: the same split, 3 .. 5: 64, 32, 16 rows by 128, split
-    int stages, splits;
+// The tiles, their stages of 128 k timed on products of 100 to 2000 rows.  Tiles of 32 rows
+// always leave sums to join.  Binary32 results have no tile of 256 x 256: their 16-bit
+// fragments do not fit its registers.
+enum { kTile256, kTile128, kTile64, kTile32, kRows32, kRows16 };
+constexpr TileCost kCosts[] = {
+    {256, 256, 1, 1.25f, 1.73f, true, false},
+    {128, 128, 2, 0.57f, 0.85f, true, true},
+    {64, 128, 2, 0.36f, 0.66f, true, true},
+    {32, 128, 2, 0.31f, 0.50f, false, true},
 };
 
-// As for the 16-bit products: the largest tile that still gives most CUs one, then smaller
-// ones, then the k range split too; few rows take a tile of as few.  wide: binary32
-// results, whose 16-bit fragments do not fit the largest tile's registers.
+// Up to 16 rows go straight from memory: 7168 x 8192, bf16, one row 12.1 us (a 16-row tile
+// of split k and its join 14.0); with 16 weight rows a workgroup every one reads all of x,
+// so from 5 rows on it takes 32 (8 rows 14.1 against 13.5 us, 16 rows 16.6 against 14.5, one
+// row 12.1 against 13.0).
 Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
     const int64_t stages = ceil_div(k, kScaleBlock);
-    if (!wide && m > 64 && ceil_div(m, 256) * ceil_div(n, 256) >= kCus * 3 / 4) return {0, (int)stages, 1};
-    const int64_t rows = m > 64 ? 128 : m > 32 ? 64 : m > 16 ? 32 : 16;
-    const int64_t tiles = ceil_div(m, rows) * ceil_div(n, 128);
-    int64_t splits = 2 * kCus / tiles;
-    if (splits > stages / 4) splits = stages / 4;
-    if (splits < 1) splits = 1;
-    const int64_t each = ceil_div(stages, splits);
-    splits = ceil_div(stages, each);
-    if (rows == 128) return {splits > 1 ? 2 : 1, (int)each, (int)splits};
-    return {rows == 64 ? 3 : rows == 32 ? 4 : 5, (int)each, (int)splits};
+    if (m <= 16) return {m <= 4 ? kRows16 : kRows32, 0, 1, false};
+    if (m <= 32) {
+        constexpr TileCost few[] = {kCosts[kTile64], kCosts[kTile32]};
+        Choice c = pick(few, m, n, stages);
+        c.tile += kTile64;
+        return c;
+    }
+    if (wide) {
+        constexpr TileCost some[] = {kCosts[kTile128], kCosts[kTile64]};
+        Choice c = pick(some, m, n, stages);
+        c.tile += kTile128;
+        return c;
+    }
+    constexpr TileCost all[] = {kCosts[kTile256], kCosts[kTile128], kCosts[kTile64]};
+    return pick(all, m, n, stages);
 }
 
 size_t part_bytes(int64_t m, int64_t n, int64_t k, bool wide) {
     const Choice c = choose(m, n, k, wide);
-    return c.tile >= 2 ? (size_t)(c.splits * m * n * 4) : 0;
+    return c.split ? (size_t)(c.splits * m * n * 4) : 0;
 }
 
 template <class Tile, int THREADS, int PER_EU>
@@ -426,14 +519,24 @@ coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, c
         using T = decltype(t);
         constexpr bool WIDE = decltype(wide)::value;
         switch (c.tile) {
-            case 0:
+            case kTile256:
                 if constexpr (!WIDE) launch_tile<Fp8Tile<T, WIDE, 8, 4, 2, 4, 2, false>, 512, 2>(p, c, stream);
                 break;
-            case 1: launch_tile<Fp8Tile<T, WIDE, 4, 4, 2, 2, 2, false>, 256, 2>(p, c, stream); break;
-            case 2: launch_tile<Fp8Tile<float, WIDE, 4, 4, 2, 2, 2, true>, 256, 2>(p, c, stream); break;
-            case 3: launch_tile<Fp8Tile<float, WIDE, 4, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
-            case 4: launch_tile<Fp8Tile<float, WIDE, 2, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
-            default: launch_tile<Fp8Tile<float, WIDE, 1, 2, 1, 4, 4, true>, 256, 2>(p, c, stream); break;
+            case kTile128:
+                if (c.split)
+                    launch_tile<Fp8Tile<float, WIDE, 4, 4, 2, 2, 2, true>, 256, 2>(p, c, stream);
+                else
+                    launch_tile<Fp8Tile<T, WIDE, 4, 4, 2, 2, 2, false>, 256, 2>(p, c, stream);
+                break;
+            case kTile64:
+                if (c.split)
+                    launch_tile<Fp8Tile<float, WIDE, 2, 2, 2, 4, 3, true>, 512, 4>(p, c, stream);
+                else
+                    launch_tile<Fp8Tile<T, WIDE, 2, 2, 2, 4, 3, false>, 512, 4>(p, c, stream);
+                break;
+            case kTile32: launch_tile<Fp8Tile<float, WIDE, 2, 2, 1, 4, 3, true>, 256, 2>(p, c, stream); break;
+            case kRows32: fp8_rows<T, WIDE, 2, 16><<<dim3((uint32_t)ceil_div(n, 32)), dim3(1024), 0, stream>>>(p); break;
+            default: fp8_rows<T, WIDE, 1, 8><<<dim3((uint32_t)ceil_div(n, 16)), dim3(512), 0, stream>>>(p); break;
         }
     };
     if (dt == COC_F32)
@@ -443,11 +546,13 @@ coc_status coc_matmul_fp8(const void* x, const float* x_scales, const void* w, c
     else
         go(bf16_t(), std::false_type());
     st = launched("matmul_fp8");
-    if (st != COC_OK || c.tile < 2) return st;
+    if (st != COC_OK || !c.split) return st;
     by_out([&](auto t) {
         using T = decltype(t);
-        fp8_join<T><<<dim3((uint32_t)ceil_div(m * ceil_div(n, 4), 256)), dim3(256), 0, stream>>>((const float*)ws, (T*)y,
-                                                                                                 m, (int)n, c.splits);
+        by_splits(c.splits, [&](auto u) {
+            fp8_join<T, decltype(u)::value><<<dim3((uint32_t)ceil_div(m * ceil_div(n, 4), 256)), dim3(256), 0, stream>>>(
+                (const float*)ws, (T*)y, m, (int)n, c.splits);
+        });
     });
     return launched("matmul_fp8 join");
 }
