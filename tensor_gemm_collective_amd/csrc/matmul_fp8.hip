@@ -71,14 +71,17 @@ struct Fp8Tile {
     using B = Operand<BN, false, NW, 1>;
     static constexpr int XW = BM > 64 ? BM / 64 : 1;   // waves that load x's scales; the others load w's
     static constexpr int SCALES = (XW + 1) * 256;      // bytes: 64 a wave
-    static constexpr int SLOT = A::BYTES + B::BYTES + SCALES;
-    static constexpr int LDS = S * SLOT;
+    static constexpr int SLOT = A::BYTES + B::BYTES;
+    static constexpr int SCALE_SLOTS = S == 2 ? 4 : 8;   // they are read until a stage's end and loaded before it
+    static constexpr int LDS = S * SLOT + SCALE_SLOTS * SCALES;
     static constexpr int DPW = A::PER_WAVE + B::PER_WAVE + 1;
     // whether a stage's loads go in two parts (see stage): with as many waves as row
     // blocks, load i of the rows is the lower half of the waves' blocks for even i
-    static constexpr bool HALVES = FI == NW;
-    static constexpr int EARLY = HALVES ? B::PER_WAVE + A::PER_WAVE / 2 : 0;
+    static constexpr bool HALVES = FI == NW && S == 2;
+    static constexpr int LATE = HALVES ? A::PER_WAVE / 2 : 0, EARLY = DPW - LATE;   // loads of each part
     static constexpr bool STAGED = !PART && sizeof(T) == 2;   // rows go out through the LDS
+    static constexpr int RING = FI >= 4 ? 4 : 2, AHEAD = FI >= 4 ? 2 : 1;   // row fragments held, and read ahead
+    static_assert(FI == 1 || FI % RING == 0, "a block's place is the same in every stage");
     static_assert(BN % kScaleBlock == 0 && kScaleBlock % (FJ * 16) == 0, "a wave's columns share a scale");
     static_assert(XW < NW, "a wave for w's scales");
     static_assert(!STAGED || BM * BN * 2 <= LDS, "the staged output fits in the LDS");
@@ -104,20 +107,21 @@ struct Fp8Tile {
                                                               p.blocks);
         const int64_t scale_step = of_x ? (int64_t)p.m * 4 : 4;
         const uint8_t* scale_base = (const uint8_t*)(of_x ? p.xs : p.ws) + stage0 * scale_step;
-        const uint32_t scale_lds = lds0 + A::BYTES + B::BYTES + (of_x ? wave : XW) * 256;
+        const uint32_t scale_lds = lds0 + S * SLOT + (of_x ? wave : XW) * 256;
+        // load d of stage s: the columns, the rows (the even loads of them), the scales, the odd loads
         auto load = [&](int d, int s, int slot, auto WHOLE) {
             constexpr bool whole = decltype(WHOLE)::value;
+            constexpr int NC = B::PER_WAVE, NR = A::PER_WAVE - LATE;
             const int left = p.k - (stage0 + s) * kScaleBlock;
-            // the columns, the even loads of the rows, the odd ones, the scales
-            constexpr int NB_ = B::PER_WAVE, NE = HALVES ? A::PER_WAVE / 2 : 0;
-            if (d < NB_)
+            if (d < NC)
                 b.template load<whole>(d, s, slot * SLOT, left);
-            else if (d < NB_ + A::PER_WAVE)
-                a.template load<whole>(!HALVES ? d - NB_ : d < NB_ + NE ? 2 * (d - NB_) : 2 * (d - NB_ - NE) + 1, s,
-                                       slot * SLOT, left);
-            else
+            else if (d < NC + NR)
+                a.template load<whole>(HALVES ? 2 * (d - NC) : d - NC, s, slot * SLOT, left);
+            else if (d == NC + NR)
                 load_lds4(scale_off, scale_base + s * scale_step,
-                          __builtin_amdgcn_readfirstlane(scale_lds + slot * SLOT));
+                          __builtin_amdgcn_readfirstlane(scale_lds + (s & (SCALE_SLOTS - 1)) * SCALES));
+            else
+                a.template load<whole>(2 * (d - EARLY) + 1, s, slot * SLOT, left);
         };
 
         const int ra = wm * FI * 16 + (lane & 15), rb = wn * FJ * 16 + (lane & 15);
@@ -141,12 +145,10 @@ struct Fp8Tile {
         auto read_b = [&](int slot, int j) {
             return fragment(slot * SLOT + pb[0] + j * 2048, slot * SLOT + pb[1] + j * 2048);
         };
-        auto read_scale = [&](int slot, int i) {
-            return *(const COC_LDS float*)(lds + slot * SLOT + A::BYTES + B::BYTES + (ra + i * 16) * 4);
-        };
-        auto read_w_scale = [&](int slot) {
-            return *(const COC_LDS float*)(lds + slot * SLOT + A::BYTES + B::BYTES + XW * 256 +
-                                           (NB > 1 ? wn * FJ * 16 / kScaleBlock * 4 : 0));
+        auto scales_at = [&](int kt) { return lds + S * SLOT + (kt & (SCALE_SLOTS - 1)) * SCALES; };
+        auto read_scale = [&](int kt, int i) { return *(const COC_LDS float*)(scales_at(kt) + (ra + i * 16) * 4); };
+        auto read_w_scale = [&](int kt) {
+            return *(const COC_LDS float*)(scales_at(kt) + XW * 256 + (NB > 1 ? wn * FJ * 16 / kScaleBlock * 4 : 0));
         };
 
         f32x4 acc[FI][FJ];
@@ -159,76 +161,79 @@ struct Fp8Tile {
 #pragma unroll
             for (int d = 0; d < DPW; ++d) load(d, s, s, std::false_type());
         if (KT >= S)
-            wait_loads<(S - 1) * DPW>();
+            wait_loads<(S - 1) * DPW + LATE>();
         else
             wait_loads<0>();
         group_barrier();
-        Values<WIDE> fa[2], fb[FJ];
+        Values<WIDE> fa[RING], fb[FJ];
 #pragma unroll
         for (int j = 0; j < FJ; ++j) fb[j] = read_b(0, j);
-        fa[0] = read_a(0, 0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) fa[i] = read_a(0, i);
 
-        // One stage.  The next row block's fragment is read under this one's MFMAs; before
-        // the last row block the workgroup meets (every wave has read this slot, and the
-        // next stage has arrived), and under its MFMAs the next stage's first fragments are
-        // read and stage kt + S is loaded into this slot.  HALVES: the workgroup also meets
-        // half way, when the columns and the lower row blocks have been read, and loads
-        // their places then: half a stage more to arrive in, and loads that do not come in
-        // one burst.
+        // One stage.  A row block's fragment is read AHEAD blocks before its MFMAs.  As many
+        // before the stage's end the workgroup meets (every wave has read this slot, and the
+        // next stage has arrived); the next stage's first fragments are read then, and stage
+        // kt + S is loaded into this slot.  HALVES: the workgroup also meets half a stage
+        // before that.  The columns and the lower row blocks have been read by then, and
+        // their places are loaded; the upper row blocks, loaded from the other meeting on,
+        // need not have arrived before.  So every load has one and a half stages to arrive
+        // in, and they do not come in one burst.
         auto stage = [&](int kt, int slot, auto MORE, auto LOAD, auto WHOLE, auto WAIT) {
             constexpr bool more = decltype(MORE)::value, loads = decltype(LOAD)::value;
-            constexpr int N = FI * FJ, HALF = N / 2, LAST = N - FJ;
+            constexpr int N = FI * FJ, LAST = N - AHEAD * FJ, MEET = LAST - N / 2;
+            constexpr int FROM = HALVES ? MEET : LAST, SPAN = HALVES ? LAST - MEET : AHEAD * FJ;   // of the early loads
             const int next = slot + 1 == S ? 0 : slot + 1;
-            f32x4 sum[3];     // of the last three MFMAs
+            constexpr int BEHIND = FJ >= 4 ? 3 : 1;   // MFMAs between one and the adding of its sums
+            f32x4 sum[BEHIND + 1];   // of the last MFMAs
             float sx[2];
-            const float sw = read_w_scale(slot);
-            sx[0] = read_scale(slot, 0);
+            const float sw = read_w_scale(kt);
+            sx[0] = read_scale(kt, 0);
             auto add = [&](int t) {
                 const int i = t / FJ, j = t % FJ;
                 const float s = sx[i & 1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sum[t % 3][e], s, acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sum[t % (BEHIND + 1)][e], s, acc[i][j][e]);
                 asm volatile("" : "+v"(acc[i][j]));   // here, not at the end of the stage
             };
 #pragma unroll
             for (int t = 0; t < N; ++t) {
                 const int i = t / FJ, j = t % FJ;
-                if (HALVES && loads && t == HALF) {
-                    wait_loads<63>();
+                if (HALVES && t == MEET) {
+                    wait_loads<decltype(WAIT)::value>();
                     group_barrier();
                 }
                 if (more && t == LAST) {
                     wait_loads<decltype(WAIT)::value>();
                     group_barrier();
                 }
-                sum[t % 3] = mfma_block(fb[j], fa[i & 1]);
-                if (t >= 2) add(t - 2);
-                if (t % FJ == (FJ > 1 ? 1 : 0)) sx[i & 1] *= sw;   // (the row block's sums are added from here on)
-                if (i + 1 < FI) {
-                    if (j == 0) fa[(i + 1) & 1] = read_a(slot, i + 1);
-                    if (j + 1 == FJ) sx[(i + 1) & 1] = read_scale(slot, i + 1);
-                } else {
-                    if constexpr (more) {
-                        fb[j] = read_b(next, j);
-                        if (j + 1 == FJ) fa[0] = read_a(next, 0);
-                    }
+                sum[t % (BEHIND + 1)] = mfma_block(fb[j], fa[i % RING]);
+                if (j == BEHIND) sx[i & 1] *= sw;   // the block's first sums come now
+                if (t >= BEHIND) add(t - BEHIND);
+                if (j + 1 == FJ && i + 1 < FI) sx[(i + 1) & 1] = read_scale(kt, i + 1);
+                if (i + AHEAD < FI) {
+                    if (j == 0) fa[(i + AHEAD) % RING] = read_a(slot, i + AHEAD);
+                } else if (more) {
+                    if (j == 0) fa[(i + AHEAD) % RING] = read_a(next, i + AHEAD - FI);
                 }
+                if (more && i + 1 == FI) fb[j] = read_b(next, j);
                 if constexpr (loads) {
 #pragma unroll
                     for (int d = 0; d < DPW; ++d)
-                        if (d < EARLY ? d * (LAST - HALF) / (EARLY > 0 ? EARLY : 1) + HALF == t
-                                      : (d - EARLY) * FJ / (DPW - EARLY) + LAST == t)
+                        if ((d < EARLY ? d * SPAN / EARLY + FROM : (d - EARLY) * AHEAD * FJ / (LATE > 0 ? LATE : 1) + LAST) == t)
                             load(d, kt + S, slot, WHOLE);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            add(N - 2);
-            add(N - 1);
+#pragma unroll
+            for (int t = N - BEHIND; t < N; ++t) add(t);
         };
         using yes = std::true_type;
         using no = std::false_type;
         int kt = 0, slot = 0;
-        using all = std::integral_constant<int, (S - 2) * DPW + EARLY>;
+        // in flight when the workgroup meets; HALVES: at either meeting, those issued since the
+        // ones it needs, half a stage's and half a stage's
+        using all = std::integral_constant<int, HALVES ? DPW : (S - 2) * DPW>;
         using none = std::integral_constant<int, 0>;
         auto step = [&] { slot = slot + 1 == S ? 0 : slot + 1; };
         // the last stage alone may be short of k
@@ -399,7 +404,7 @@ __global__ __launch_bounds__(256) void fp8_join(const float* part, T* y, int64_t
 enum { kTile256, kTile128, kTile64, kTile32, kRows32, kRows16 };
 constexpr TileCost kCosts[] = {
     {256, 256, 1, 1.25f, 1.73f, true, false},
-    {128, 128, 2, 0.57f, 0.85f, true, true},
+    {128, 128, 2, 0.57f, 0.95f, true, true},
     {64, 128, 2, 0.36f, 0.66f, true, true},
     {32, 128, 2, 0.31f, 0.50f, false, true},
 };
