@@ -58,17 +58,16 @@ __global__ __launch_bounds__(256) void fill_zeros(T* p, int64_t vectors) {
 // ------------------------------------------------------------------ which tile
 // The tiles, their stages of 64 k timed on products of 100 to 1500 rows.  The largest reads
 // its operands least often.  128 x 128 comes with four slots, one workgroup a CU, for
-// products of few tiles, and with two slots and two workgroups a CU.  Tiles of few rows are
-// a pass over the weights and always leave sums to join.
-enum { kTile256, kTile128Deep, kTile128, kTile64, kTile32, kTile16, kTiles };
-constexpr TileCost kCosts[kTiles] = {
-    {256, 256, 1, 1.35f, 1.50f, true, false}, {128, 128, 1, 0.55f, 0.55f, true, false},
-    {128, 128, 2, 0.84f, 0.94f, true, true},  {64, 128, 2, 0.38f, 0.80f, true, true},
-    {32, 128, 2, 0.40f, 0.60f, false, true},  {16, 128, 2, 0.36f, 0.50f, false, true},
+// products of few tiles, and with two slots and two workgroups a CU.
+enum { kTile256, kTile128Deep, kTile128, kTile64, kTile32, kTile16 };
+constexpr TileCost kCosts[] = {
+    {256, 256, 1, 1.35f, 1.50f, 6.0f, true, false}, {128, 128, 1, 0.55f, 0.55f, 3.0f, true, false},
+    {128, 128, 2, 0.84f, 0.94f, 3.0f, true, true},  {64, 128, 2, 0.38f, 0.80f, 2.0f, true, true},
+    {32, 128, 2, 0.40f, 0.60f, 1.5f, true, true},   {16, 128, 2, 0.36f, 0.50f, 1.5f, true, true},
 };
 
 // m x n outputs (n: f of the gated product, whose tiles hold twice as many columns of B).
-// Up to 32 rows take a tile of as few and two workgroups a CU.
+// Up to 32 rows take a tile of as few.  ta: A is stored k-major, in chunks of 8 rows.
 Choice choose(int64_t m, int64_t n, int64_t k, bool gated, bool ta) {
     const int64_t cols = gated ? 2 * n : n, stages = ceil_div(k, 64);
     if (m > 32 || ta) {
@@ -96,8 +95,7 @@ void launch_tile(MmParams p, const Choice& c, hipStream_t stream) {
 
 // C = A B of these sizes by the chosen tile, joined where it is split.
 template <class T, bool TA, bool TB, bool GATED>
-coc_status product(MmParams p, hipStream_t stream) {
-    const Choice c = choose(p.m, p.n, p.k, GATED, TA);
+coc_status product(MmParams p, const Choice& c, hipStream_t stream) {
     switch (c.tile) {
         case kTile256: launch_tile<MmTile<T, TA, TB, 8, 4, 2, 4, 2, GATED, false>>(p, c, stream); break;
         case kTile128Deep: launch_tile<MmTile<T, TA, TB, 4, 2, 2, 4, 4, GATED, false>>(p, c, stream); break;
@@ -114,10 +112,20 @@ coc_status product(MmParams p, hipStream_t stream) {
                 launch_tile<MmTile<T, TA, TB, 2, 2, 2, 4, 3, GATED, false>>(p, c, stream);
             break;
         case kTile32:
-            if constexpr (!TA) launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, true>>(p, c, stream);
+            if constexpr (!TA) {
+                if (c.split)
+                    launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, true>>(p, c, stream);
+                else
+                    launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, false>>(p, c, stream);
+            }
             break;
         default:
-            if constexpr (!TA) launch_tile<MmTile<T, TA, TB, 1, 2, 1, 4, 4, GATED, true>>(p, c, stream);
+            if constexpr (!TA) {
+                if (c.split)
+                    launch_tile<MmTile<T, TA, TB, 1, 2, 1, 4, 4, GATED, true>>(p, c, stream);
+                else
+                    launch_tile<MmTile<T, TA, TB, 1, 2, 1, 4, 4, GATED, false>>(p, c, stream);
+            }
             break;
     }
     coc_status st = launched("gated feed-forward product");
@@ -128,6 +136,85 @@ coc_status product(MmParams p, hipStream_t stream) {
                 p.part, (T*)p.c, (T*)p.gate_up, p.m, p.n, c.splits, p.act);
     });
     return launched("gated feed-forward join");
+}
+
+// The backward pass's two products, dx (m x d over 2f) and dw (d x 2f over m), in one
+// launch of the same tile: their workgroups fill the rounds together, where each alone
+// leaves a round partly empty, and a small pass is spared a launch.  The longer tiles go
+// first.
+template <class X, class W>
+__global__ __launch_bounds__(X::NW * 64, kWavesSimd<X>) void mm_pair(MmParams x, MmParams w, int x0, int w0) {
+    static_assert(X::NW == W::NW && X::LDS == W::LDS, "one launch for both");
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[X::LDS];
+    const int b = (int)blockIdx.x;
+    if (b >= x0 && (x0 >= w0 || b < w0))
+        X::run(x, sm, b - x0);
+    else
+        W::run(w, sm, b - w0);
+}
+
+struct Pair {
+    int tile;   // -1: each by itself
+    float us;
+};
+Pair choose_pair(int64_t m, int64_t d, int64_t f) {
+    const int64_t sx = ceil_div(2 * f, 64), sw = ceil_div(m, 64);
+    Pair best{-1, choose(m, d, 2 * f, false, false).us + choose(d, 2 * f, m, false, true).us + 4.0f};
+    for (int t : {kTile256, kTile128Deep, kTile128, kTile64}) {
+        const TileCost& c = kCosts[t];
+        const int64_t tx = ceil_div(m, c.rows) * ceil_div(d, c.cols), tw = ceil_div(d, c.rows) * ceil_div(2 * f, c.cols);
+        const int64_t slots = kCus * c.per_cu;
+        const float stage = tx + tw <= kCus ? c.light : c.full;
+        // evenly shared, but for the last tiles' half; at least the longest tile
+        const float longest = (float)(sx > sw ? sx : sw) * stage + c.ends;
+        float us = ((float)(tx * sx + tw * sw) * stage + (float)(tx + tw) * c.ends) / (float)slots;
+        us = tx + tw <= slots ? longest : us + 0.5f * ((float)(sx < sw ? sx : sw) * stage + c.ends);
+        if (us < longest) us = longest;
+        if (us < best.us) best = {t, us};
+    }
+    return best;
+}
+
+// One of them alone takes the tile without a split too, so that it has the same bits (each
+// output adds its products in the order of k, whatever the tile; a split adds sums).
+Choice unsplit(int64_t m, int64_t n, int64_t k) {
+    TileCost whole[4];
+    for (int t = 0; t < 4; ++t) {
+        whole[t] = kCosts[t];
+        whole[t].split = false;
+    }
+    return pick(whole, m, n, ceil_div(k, 64));
+}
+
+template <class X, class W>
+void launch_pair(MmParams x, MmParams w, hipStream_t stream) {
+    for (MmParams* p : {&x, &w}) {
+        p->tiles_m = (int)ceil_div(p->m, X::BM);
+        p->tiles_n = (int)ceil_div(p->n, X::BN);
+        p->stages = (int)ceil_div(p->k, 64);
+    }
+    const int tx = x.tiles_m * x.tiles_n, tw = w.tiles_m * w.tiles_n;
+    const bool x_first = x.stages >= w.stages;
+    mm_pair<X, W><<<dim3((uint32_t)(tx + tw)), dim3(X::NW * 64), 0, stream>>>(x, w, x_first ? 0 : tw, x_first ? tx : 0);
+}
+
+template <class T>
+coc_status product_pair(int tile, const MmParams& x, const MmParams& w, hipStream_t stream) {
+    switch (tile) {
+        case kTile256:
+            launch_pair<MmTile<T, false, true, 8, 4, 2, 4, 2, false, false>, MmTile<T, true, false, 8, 4, 2, 4, 2, false, false>>(x, w, stream);
+            break;
+        case kTile128Deep:
+            launch_pair<MmTile<T, false, true, 4, 2, 2, 4, 4, false, false>, MmTile<T, true, false, 4, 2, 2, 4, 4, false, false>>(x, w, stream);
+            break;
+        case kTile128:
+            launch_pair<MmTile<T, false, true, 4, 4, 2, 2, 2, false, false>, MmTile<T, true, false, 4, 4, 2, 2, 2, false, false>>(x, w, stream);
+            break;
+        default:
+            launch_pair<MmTile<T, false, true, 2, 2, 2, 4, 3, false, false>, MmTile<T, true, false, 2, 2, 2, 4, 3, false, false>>(x, w, stream);
+            break;
+    }
+    return launched("gated feed-forward backward");
 }
 
 template <class F>
@@ -167,7 +254,7 @@ coc_status gated_product(const void* x, const void* w, void* h, void* gate_up, i
     p.gate_up = gate_up;
     p.act = act;
     p.part = (float*)part;
-    return by_type16(dt, [&](auto t) { return product<decltype(t), false, false, true>(p, stream); });
+    return by_type16(dt, [&](auto t) { return product<decltype(t), false, false, true>(p, choose(m, f, d, true, false), stream); });
 }
 
 struct BackwardSpace {
@@ -259,19 +346,20 @@ coc_status coc_gated_ffn_backward(const void* dh, const void* x, const void* w, 
     if (st != COC_OK) return st;
     return by_type16(dt, [&](auto t) {
         using T = decltype(t);
+        MmParams x_ = operands(dgu, 2 * f, w, 2 * f, m, d, 2 * f), w_ = operands(x, d, dgu, 2 * f, d, 2 * f, m);
+        x_.c = dx;
+        w_.c = dw;
+        x_.part = w_.part = (float*)part;
+        const Pair pair = choose_pair(m, d, f);
+        const bool whole = pair.tile >= 0;
+        if (whole && dx && dw) return product_pair<T>(pair.tile, x_, w_, stream);
         coc_status s = COC_OK;
-        if (dx) {
-            MmParams p = operands(dgu, 2 * f, w, 2 * f, m, d, 2 * f);
-            p.c = dx;
-            p.part = (float*)part;
-            s = product<T, false, true, false>(p, stream);
-        }
-        if (s == COC_OK && dw) {
-            MmParams p = operands(x, d, dgu, 2 * f, d, 2 * f, m);
-            p.c = dw;
-            p.part = (float*)part;
-            s = product<T, true, false, false>(p, stream);
-        }
+        if (dx)
+            s = product<T, false, true, false>(x_, whole ? unsplit(m, d, 2 * f) : choose(m, d, 2 * f, false, false),
+                                               stream);
+        if (s == COC_OK && dw)
+            s = product<T, true, false, false>(w_, whole ? unsplit(d, 2 * f, m) : choose(d, 2 * f, m, false, true),
+                                               stream);
         return s;
     });
 }

@@ -153,12 +153,13 @@ struct Operand {
 constexpr int64_t kCus = 256;   // of an MI355X
 
 // A tile as measured: its rows and columns (of the operands), the workgroups a CU holds,
-// and the time of a stage in us while there is at most one workgroup a CU (`light`) and
-// while there are more (`full`).  Whether it may be split along k.
+// the time of a stage in us while there is at most one workgroup a CU (`light`) and while
+// there are more (`full`), and of a tile's start and end (`ends`).  Whether it is offered
+// whole, and split along k.
 struct TileCost {
     int rows, cols, per_cu;
-    float light, full;
-    bool whole, split;   // offered unsplit, offered split
+    float light, full, ends;
+    bool whole, split;
 };
 
 struct Choice {
@@ -166,6 +167,7 @@ struct Choice {
     int stages;   // of one split
     int splits;   // 1: not split
     bool split;   // leaves sums for a joining kernel
+    float us;     // estimated
 };
 
 // The tile and split of the least estimated time for an m x n product of `stages` stages:
@@ -173,8 +175,7 @@ struct Choice {
 // launches, and its sums written and read at 6 TB/s).
 template <int N>
 inline Choice pick(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t stages) {
-    Choice best{0, (int)stages, 1, false};
-    float least = 1e30f;
+    Choice best{0, (int)stages, 1, false, 1e30f};
     for (int t = 0; t < N; ++t) {
         const TileCost& c = costs[t];
         const int64_t tiles = ceil_div(m, c.rows) * ceil_div(n, c.cols);
@@ -184,12 +185,10 @@ inline Choice pick(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t sta
             if (s > 1 && (each < 2 || ceil_div(stages, each) != s)) continue;
             const bool join = s > 1 || !c.whole;
             const int64_t groups = tiles * s;
-            float us = (float)ceil_div(groups, kCus * c.per_cu) * (float)each * (groups <= kCus ? c.light : c.full);
+            float us = (float)ceil_div(groups, kCus * c.per_cu) *
+                       ((float)each * (groups <= kCus ? c.light : c.full) + c.ends);
             if (join) us += 5.0f + (float)(s * m * n) * (8.0f / 6e6f);
-            if (us < least) {
-                least = us;
-                best = {t, (int)each, (int)s, join};
-            }
+            if (us < best.us) best = {t, (int)each, (int)s, join, us};
             if (groups > 4 * kCus * c.per_cu) break;
         }
     }

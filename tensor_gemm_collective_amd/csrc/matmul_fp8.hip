@@ -403,10 +403,10 @@ __global__ __launch_bounds__(256) void fp8_join(const float* part, T* y, int64_t
 // fragments do not fit its registers.
 enum { kTile256, kTile128, kTile64, kTile32, kRows32, kRows16 };
 constexpr TileCost kCosts[] = {
-    {256, 256, 1, 1.25f, 1.73f, true, false},
-    {128, 128, 2, 0.57f, 0.95f, true, true},
-    {64, 128, 2, 0.36f, 0.66f, true, true},
-    {32, 128, 2, 0.31f, 0.50f, false, true},
+    {256, 256, 1, 1.25f, 1.65f, 4.0f, true, false},
+    {128, 128, 2, 0.57f, 0.95f, 2.5f, true, true},
+    {64, 128, 2, 0.36f, 0.66f, 1.5f, true, true},
+    {32, 128, 2, 0.31f, 0.50f, 1.2f, false, true},
 };
 
 // Up to 16 rows go straight from memory: 7168 x 8192, bf16, one row 12.1 us (a 16-row tile
@@ -415,7 +415,7 @@ constexpr TileCost kCosts[] = {
 // row 12.1 against 13.0).
 Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
     const int64_t stages = ceil_div(k, kScaleBlock);
-    if (m <= 16) return {m <= 4 ? kRows16 : kRows32, 0, 1, false};
+    if (m <= 16) return {m <= 4 ? kRows16 : kRows32, 0, 1, false, 0.0f};
     if (m <= 32) {
         constexpr TileCost few[] = {kCosts[kTile64], kCosts[kTile32]};
         Choice c = pick(few, m, n, stages);

@@ -93,9 +93,10 @@ struct MmTile {
     static constexpr int RPM = (NRD + NMM - BAR_AT - 1) / (NMM - BAR_AT);   // reads an MFMA
     static_assert(PART || NW * FI * 16 * FJ * 32 <= LDS, "the staged output fits in the LDS");
 
-    static __device__ __forceinline__ void run(const MmParams& p, uint8_t* sm) {
+    // block: the tile's number, of the launch's or of this product's
+    static __device__ __forceinline__ void run(const MmParams& p, uint8_t* sm, int block) {
         int tm, tn;
-        tile_of(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn);
+        tile_of(block, p.tiles_m, p.tiles_n, &tm, &tn);
         const int m0 = tm * BM, n0 = tn * OUT;
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int wm = wave / WN, wn = wave % WN;
@@ -236,7 +237,7 @@ struct MmTile {
             COC_LDS uint8_t* stg = (COC_LDS uint8_t*)sm + wave * (FI * 16 * FJ * 32);
             auto put = [&](auto COLS, auto&& value, uint8_t* c, int64_t ld, int64_t col_of, int col0) {
                 constexpr int NJ = decltype(COLS)::value, PITCH = NJ * 32, CPR = NJ * 2, RPI = 64 / CPR;
-                static_assert(64 % CPR == 0 && (FI * 16) % RPI == 0, "staging layout");
+                static_assert(64 % CPR == 0, "staging layout");
 #pragma unroll
                 for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -248,8 +249,9 @@ struct MmTile {
                     }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < FI * 16 / RPI; ++t) {
+                for (int t = 0; t < (FI * 16 + RPI - 1) / RPI; ++t) {
                     const int row = t * RPI + lane / CPR, ch = lane % CPR;
+                    if (FI * 16 % RPI != 0 && row >= FI * 16) continue;
                     const u32x4 v = *(const COC_LDS u32x4*)(stg + row * PITCH + ((ch ^ (row & (CPR - 1))) << 4));
                     const int r = m0 + wm * FI * 16 + row, col = col0 + ch * 8;
                     if (r < p.m && col < p.n) *(u32x4*)(c + (r * ld + col_of + col) * 2) = v;
@@ -291,7 +293,7 @@ constexpr int kWavesSimd = (Tile::LDS > 80 * 1024 ? 1 : 2) * Tile::NW / 4;
 template <class Tile>
 __global__ __launch_bounds__(Tile::NW * 64, kWavesSimd<Tile>) void mm_tile(MmParams p) {
     __shared__ __attribute__((aligned(1024))) uint8_t sm[Tile::LDS];
-    Tile::run(p, sm);
+    Tile::run(p, sm, (int)blockIdx.x);
 }
 
 }  // namespace

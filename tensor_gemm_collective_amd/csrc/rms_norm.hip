@@ -103,14 +103,14 @@ constexpr int kNormThreads = 512;   // of a backward workgroup, or a row's where
 //   dx = rstd (g - xh avg(g xh)) + dsum,  dgamma = sum over rows of dy xh.
 // TPR threads take a row, a thread always the same columns, so the columns' sums
 // stay in its registers over all its rows; a workgroup leaves its own as row b of
-// `part` (grid x n), which rms_backward_sum adds up in order.  While a row is
+// `part` (grid x n), which rms_backward_sum adds up in order, or a lone one in dgamma.  While a row is
 // summed the next one is on its way into the other of two sets of registers.  All
 // groups make as many steps; a row past the last is the last one again, counted
 // nowhere.
 template <class T, class W, int TPR, int EPT, RowKind KIND>
 __global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void rms_backward(
-    const T* dy, const T* x, const W* gamma, const float* rstd_in, const T* dsum, T* dx, float* part, int64_t rows,
-    int n) {
+    const T* dy, const T* x, const W* gamma, const float* rstd_in, const T* dsum, T* dx, float* part, W* dgamma,
+    int64_t rows, int n) {
     constexpr int VN = kVec<T>, V = EPT / VN;
     constexpr int THREADS = TPR < kNormThreads ? kNormThreads : TPR, GROUPS = THREADS / TPR;
     constexpr int LEFT = GROUPS > 1 ? GROUPS / 2 : 0;   // groups whose sums go through LDS at once
@@ -239,18 +239,23 @@ __global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void rms_b
             }
         }
     if (group > 0) return;
-    float* pr = part + (int64_t)blockIdx.x * n;
+    auto leave = [&](auto* to) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const Cols<T, KIND> col(v * TPR + t, n);
-        if (KIND == kTiny || col.skip == 0) {
-            keep_n<VN>(pr, col.c, n, dg[v]);
-        } else if (col.skip < VN) {
+        for (int v = 0; v < V; ++v) {
+            const Cols<T, KIND> col(v * TPR + t, n);
+            if (KIND == kTiny || col.skip == 0) {
+                keep_n<VN>(to, col.c, n, dg[v]);
+            } else if (col.skip < VN) {
 #pragma unroll
-            for (int i = 0; i < VN; ++i)
-                if (col.has(i, n)) pr[col.c + i] = dg[v][i];
+                for (int i = 0; i < VN; ++i)
+                    if (col.has(i, n)) to[col.c + i] = (std::remove_pointer_t<decltype(to)>)dg[v][i];
+            }
         }
-    }
+    };
+    if (gridDim.x == 1)
+        leave(dgamma);
+    else
+        leave(part + (int64_t)blockIdx.x * n);
 }
 
 // Sums the parts' columns: 32 columns a workgroup, its eight half-waves an eighth
@@ -287,12 +292,12 @@ __global__ __launch_bounds__(256) void rms_backward_sum(const float* part, int p
 constexpr int64_t kMaxNorm = 32768;   // elements of a row: 1024 threads of 32
 
 // Workgroups of the backward pass, one part each: a CU's worth, since the parts
-// are written and read again.
+// are written and read again.  Few rows take one, which needs no second kernel.
 constexpr int64_t kMostParts = 256;
 int64_t backward_parts(int64_t rows, int64_t n) {
     const int64_t groups = n <= 1024 ? 8 : n <= 2048 ? 4 : n <= 4096 ? 2 : 1;   // rows at a time
     const int64_t want = (rows + groups - 1) / groups;
-    return want < kMostParts ? want : kMostParts;
+    return want <= 4 ? 1 : want < kMostParts ? want : kMostParts;
 }
 
 template <RowKind K>
@@ -410,7 +415,8 @@ coc_status coc_rms_norm_fp8(const void* x, const void* residual, const void* gam
 
 size_t coc_rms_norm_backward_workspace_bytes(int64_t rows, int64_t n) {
     if (rows <= 0 || n <= 0 || n > coc::kMaxNorm) return 0;
-    return (size_t)(coc::backward_parts(rows, n) * n * 4);
+    const int64_t parts = coc::backward_parts(rows, n);
+    return parts > 1 ? (size_t)(parts * n * 4) : 0;
 }
 
 coc_status coc_rms_norm_backward(const void* dy, const void* x, const void* gamma, const float* rstd, const void* dsum,
@@ -447,12 +453,12 @@ coc_status coc_rms_norm_backward(const void* dy, const void* x, const void* gamm
                 constexpr int TPR = decltype(tpr)::value, EPT = decltype(ept)::value;
                 rms_backward<T, W, TPR, EPT, decltype(kind)::value>
                     <<<dim3((uint32_t)parts), dim3(TPR < kNormThreads ? kNormThreads : TPR), 0, stream>>>(
-                        (const T*)dy, (const T*)x, (const W*)gamma, rstd, (const T*)dsum, (T*)dx, (float*)ws, rows,
-                        (int)n);
+                        (const T*)dy, (const T*)x, (const W*)gamma, rstd, (const T*)dsum, (T*)dx, (float*)ws,
+                        (W*)dgamma, rows, (int)n);
             });
         });
         st = launched("rms norm backward");
-        if (st != COC_OK) return st;
+        if (st != COC_OK || parts == 1) return st;
     }
     // without rows the sums are 0
     by_types(param_dt, param_dt, [&](auto w, auto) {

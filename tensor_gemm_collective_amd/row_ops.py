@@ -52,6 +52,8 @@ def _ptr(t):
 
 def _want(t, name, like, dtype, *shape):
     """`t` is a dense tensor of that dtype and shape on like's device; returns its address."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != like.device:
@@ -63,7 +65,10 @@ def _want(t, name, like, dtype, *shape):
 
 def _out(t, name, like, stream, dtype, *shape):
     if t is None:
-        t = _new(shape, dtype, like, stream)
+        if stream is None and like.is_cuda:   # (sizes as arguments: quicker than as a tuple)
+            t = like.new_empty(*shape, dtype=dtype)
+        else:
+            t = _new(shape, dtype, like, stream)
         return t, t.data_ptr()
     return t, _want(t, name, like, dtype, *shape)
 

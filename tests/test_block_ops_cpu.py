@@ -56,8 +56,8 @@ CASES = [
     (rms, dict(y=at(0)), ALIAS), (rms8, dict(q=at(3) + 8), ALIGN), (rms8, dict(scales=at(4) + 2), ALIGN),
     (rms8, dict(q=at(0)), ALIAS), (rms8, dict(scales=at(3) + 64), ALIAS), (rms8, dict(n=72), SHAPE),
     (rms8, dict(rstd=at(4) + 12), ALIAS),
-    (rmsb, dict(ws=None), WORKSPACE), (rmsb, dict(nws=8), WORKSPACE), (rmsb, dict(ws=at(20) + 2), ALIGN),
-    (rmsb, dict(dx=at(0)), ALIAS), (rmsb, dict(ws=at(5)), ALIAS), (rmsb, dict(pdt=1), DTYPE), (rmsb, dict(n=32769), SHAPE),
+    (rmsb, dict(rows=100, ws=None), WORKSPACE), (rmsb, dict(rows=100, nws=8), WORKSPACE),
+    (rmsb, dict(rows=100, ws=at(20) + 2), ALIGN), (rmsb, dict(dx=at(0)), ALIAS), (rmsb, dict(rows=100, ws=at(5)), ALIAS), (rmsb, dict(pdt=1), DTYPE), (rmsb, dict(n=32769), SHAPE),
     (rmsb, dict(rows=0, dgamma=None), NULL),
     *[(quant, {k: None}, NULL) for k in ("x", "q", "scales")],
     (quant, dict(n=72), SHAPE), (quant, dict(rows=-1), SHAPE), (quant, dict(block_rows=2), DTYPE),
@@ -81,8 +81,8 @@ CASES = [
     *[(f, kw, s) for f in (ffn, ffnb) for kw, s in (
         (dict(dt=0), DTYPE), (dict(act=2), DTYPE), (dict(d=60), SHAPE), (dict(f=12), SHAPE), (dict(d=0), SHAPE),
         (dict(f=0), SHAPE), (dict(m=-1), SHAPE), (dict(d=1 << 16, f=1 << 15), SHAPE), (dict(f=1 << 31), SHAPE),
-        (dict(x=at(1) + 8), ALIGN), (dict(gate_up=at(3) + 2), ALIGN), (dict(ws=None), WORKSPACE),
-        (dict(nws=64), WORKSPACE), (dict(ws=at(20) + 8), ALIGN), (dict(ws=at(3)), ALIAS))],
+        (dict(x=at(1) + 8), ALIGN), (dict(gate_up=at(3) + 2), ALIGN), (dict(d=8192, ws=None), WORKSPACE),
+        (dict(d=8192, nws=64), WORKSPACE), (dict(d=8192, ws=at(20) + 8), ALIGN), (dict(d=8192, ws=at(3)), ALIAS))],
     (ffn, dict(h=at(1)), ALIAS), (ffn, dict(gate_up=at(2) + 240), ALIAS), (ffnb, dict(dx=at(1)), ALIAS),
     (ffnb, dict(dw=at(2)), ALIAS), (ffnb, dict(dw=at(4)), ALIAS),
 ]
@@ -109,7 +109,8 @@ def test_calls_without_rows_do_nothing():
 def test_workspace_sizes():
     L = tgc.lib()
     assert L.coc_rms_norm_backward_workspace_bytes(0, 64) == 0
-    assert L.coc_rms_norm_backward_workspace_bytes(3, 64) >= 64 * 4
+    assert L.coc_rms_norm_backward_workspace_bytes(3, 64) == 0          # one workgroup
+    assert L.coc_rms_norm_backward_workspace_bytes(300, 64) >= 2 * 64 * 4
     assert L.coc_rms_norm_backward_workspace_bytes(3, 32769) == 0
     assert L.coc_matmul_fp8_workspace_bytes(0, 8, 16) == 0 and L.coc_matmul_fp8_workspace_bytes(8, 8, 8) == 0
     assert L.coc_gated_ffn_workspace_bytes(4, 60, 64) == 0
