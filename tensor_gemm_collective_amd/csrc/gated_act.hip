@@ -16,7 +16,7 @@ struct Place {
         : row(i / per_row), col((int)(i - (uint32_t)row * per_row), f) {}
 };
 
-// h = act(g) u, rounded once.  Memory bound: two reads and a write.
+// h = act(g) u, rounded once.  Memory bound: two reads and a write, a vector a thread.
 template <class T, int ACT, RowKind KIND>
 __global__ __launch_bounds__(256) void gated_forward(const T* gate_up, T* h, uint32_t vectors, uint32_t per_row,
                                                      int f) {
@@ -34,7 +34,8 @@ __global__ __launch_bounds__(256) void gated_forward(const T* gate_up, T* h, uin
     at.col.store(h + at.row * f, f, o);
 }
 
-// dg = dh u act'(g), du = dh act(g).  Memory bound: three reads, two writes.
+// dg = dh u act'(g), du = dh act(g).  Memory bound, three reads and two writes: 4096 x 3584
+// (bf16, 147 MB) 28 us, 5.2 TB/s.
 template <class T, int ACT, RowKind KIND>
 __global__ __launch_bounds__(256) void gated_backward(const T* dh, const T* gate_up, T* dgate_up, uint32_t vectors,
                                                       uint32_t per_row, int f) {
@@ -64,7 +65,8 @@ __global__ __launch_bounds__(256) void gated_backward(const T* dh, const T* gate
 // Rows to 8 bits with a scale for each 128 of a row (fp8.h): of x (rows x n), or
 // ACT >= 0: of act(g) u, x being rows x 2n.  A block's columns lie in 16 (32:
 // binary32) neighbouring lanes; a workgroup takes one column block of 16 (8) rows, so
-// that its scales are neighbours in memory.  n is a multiple of 16.
+// that its scales are neighbours in memory.  n is a multiple of 16.  Memory bound: act(g) u
+// of 4096 x 3584 (bf16, 74 MB) 12.9 us, 5.7 TB/s.
 template <class T, int ACT>
 __global__ __launch_bounds__(256) void quantize_rows(const T* x, uint8_t* q, float* scales, int64_t rows, int n,
                                                      int blocks) {
@@ -97,7 +99,8 @@ __global__ __launch_bounds__(256) void quantize_rows(const T* x, uint8_t* q, flo
     if (threadIdx.x % LANES == 0) scales[block * rows + row] = s.scale;
 }
 
-// A 128 x 128 block of x a workgroup, held in registers.
+// A 128 x 128 block of x a workgroup, held in registers, so that x is read once.  Memory
+// bound: 7168 x 8192 (bf16, 176 MB) 31.7 us, 5.6 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void quantize_blocks(const T* x, uint8_t* q, float* scales, int64_t rows, int n,
                                                        int blocks) {
