@@ -175,12 +175,18 @@ def _check(status: int) -> None:
 
 
 # ------------------------------------------------------------------ marshalling
+_codes = {}   # of torch's dtypes, filled by the first call
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float32: COC_F32, torch.float16: COC_F16, torch.bfloat16: COC_BF16}
-    if t.dtype not in codes:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    code = _codes.get(t.dtype)
+    if code is None:
+        import torch
+        _codes.update({torch.float32: COC_F32, torch.float16: COC_F16, torch.bfloat16: COC_BF16})
+        code = _codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _ptr(t):

@@ -38,7 +38,7 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 // Fragment reads of block `j` (16 rows or columns from row0 on), k step ks (32 k).
 template <int ROWS, bool TRANS>
 struct Fragments {
-    int place[TRANS ? 2 : 2];
+    int place[2];
     int row0;
     __device__ __forceinline__ void init(int first, int lane) {
         row0 = first;

@@ -101,6 +101,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_forward(const T* x,
 }
 
 constexpr int kNormThreads = 512;   // of a backward workgroup, or a row's where that is more
+constexpr int kSumThreads = 512;
 
 // Backward.  xh = x rstd, g = dy gamma:
 //   dx = rstd (g - xh avg(g xh)) + dsum,  dgamma = sum over rows of dy xh.
@@ -265,11 +266,12 @@ __global__ __launch_bounds__(TPR < kNormThreads ? kNormThreads : TPR) void rms_b
         leave(part + (int64_t)blockIdx.x * n);
 }
 
-// Sums the parts' columns: 32 columns a workgroup, its eight half-waves an eighth
-// of the parts each (in order), joined in order.
+// Sums the parts' columns: 32 columns a workgroup, its 16 half-waves a sixteenth of the
+// parts each (in order), joined in order.  (8 half-waves: 0.3 to 0.6 us more at 256 parts,
+// 32: the same.)
 template <class W>
-__global__ __launch_bounds__(256) void rms_backward_sum(const float* part, int parts, int n, W* dgamma) {
-    constexpr int COLS = 32, RUNS = 256 / COLS;
+__global__ __launch_bounds__(kSumThreads) void rms_backward_sum(const float* part, int parts, int n, W* dgamma) {
+    constexpr int COLS = 32, RUNS = kSumThreads / COLS;
     __shared__ float buf[RUNS][COLS];
     const int c = (int)blockIdx.x * COLS + (threadIdx.x % COLS);
     const int w = threadIdx.x / COLS;
@@ -472,7 +474,7 @@ coc_status coc_rms_norm_backward(const void* dy, const void* x, const void* gamm
     // without rows the sums are 0
     by_types(param_dt, param_dt, [&](auto w, auto) {
         using W = decltype(w);
-        rms_backward_sum<W><<<dim3((uint32_t)ceil_div(n, 32)), dim3(256), 0, stream>>>((const float*)ws, (int)parts,
+        rms_backward_sum<W><<<dim3((uint32_t)ceil_div(n, 32)), dim3(kSumThreads), 0, stream>>>((const float*)ws, (int)parts,
                                                                                       (int)n, (W*)dgamma);
     });
     return launched("rms norm backward");

@@ -16,6 +16,8 @@ from .coc import _check, _dtype_code, _stream, lib
 # torch's own quick way to the current stream's handle; current_stream() makes an
 # object for it, which takes longer than a small kernel's launch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device's number (a tensor on the GPU is there, so torch has begun with it)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on_gpu(like):
@@ -37,10 +39,11 @@ def _new(shape, dtype, like, stream):
 def _queue(stream, like):
     """The handle of the stream the call's work goes to."""
     _on_gpu(like)
-    if like.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {like.device}, the current device is {torch.cuda.current_device()}")
+    device = like.get_device()
+    if device != _device():
+        raise ValueError(f"the tensors are on {like.device}, the current device is {_device()}")
     if stream is None and _raw_stream is not None:
-        return _raw_stream(like.device.index)
+        return _raw_stream(device)
     return _stream(stream, like.device)
 
 
