@@ -111,7 +111,7 @@ constexpr int kSumThreads = 512;
 // summed the next one is on its way into the other of two sets of registers.  All
 // groups make as many steps; a row past the last is the last one again, counted
 // nowhere.  Bound by memory and the parts: 2048 x 8192 with dsum (bf16, 134 MB and
-// 8.4 MB of parts) 29.1 us, 4.9 TB/s, and 4.0 to add up the parts.  Two rows at a
+// 8.4 MB of parts) 28.5 us, 5.0 TB/s, and 4 to 5 to add up the parts.  Two rows at a
 // time in 1024 threads gained nothing there (30.2 against 30.5 us in all) and spilled
 // binary32 rows (1500 x 7000: 62 against 37 us); rows past 16384 columns spill 9 (16
 // bits) or 92 of 128 registers.
