@@ -73,24 +73,25 @@ __global__ __launch_bounds__(256) void fill_zeros(T* p, int64_t vectors) {
 // loads that keep their lines in the L1 all took the same time (non-temporal ones up to 1.8 times
 // it); on a copy whose loads all hit the L2 1024 x 2048 x 4096 took 27 of 28 us, 3313 x 304 x
 // 4056 24 of 29 and 128 x 7168 x 8192, unsplit, 41 of 81; with no loads 17, 16 and 27.
-enum { kTile256, kTile128Deep, kTile128, kTile64, kTile32, kTile16 };
+enum { kTile256, kTile128Deep, kTile128, kTile64, kTile32 };
 constexpr TileCost kCosts[] = {
     {256, 256, 1, 1.35f, 1.50f, 6.0f, true, false}, {128, 128, 1, 0.55f, 0.55f, 3.0f, true, false},
     {128, 128, 2, 0.84f, 0.94f, 3.0f, true, true},  {64, 128, 2, 0.38f, 0.80f, 2.0f, true, true},
-    {32, 128, 2, 0.40f, 0.60f, 1.5f, true, true},   {16, 128, 2, 0.36f, 0.50f, 1.5f, true, true},
+    {32, 128, 2, 0.40f, 0.60f, 1.5f, true, true},
 };
 
 // m x n outputs (n: f of the gated product, whose tiles hold twice as many columns of B).
-// Up to 32 rows take a tile of as few.  ta: A is stored k-major, in chunks of 8 rows.
+// Up to 32 rows take a tile of as few (one row through 8192 x 7168 26.2 us, by 64 x 128 26.9;
+// 16 rows 27.9 and 28.1; a tile of 16 rows took the same).  ta: A is stored k-major.
 Choice choose(int64_t m, int64_t n, int64_t k, bool gated, bool ta) {
     const int64_t cols = gated ? 2 * n : n, stages = ceil_div(k, 64);
     if (m > 32 || ta) {
         constexpr TileCost large[] = {kCosts[0], kCosts[1], kCosts[2], kCosts[3]};
         return pick(large, m, cols, stages);
     }
-    constexpr TileCost few32[] = {kCosts[kTile32]}, few16[] = {kCosts[kTile16]};
-    Choice c = m > 16 ? pick(few32, m, cols, stages) : pick(few16, m, cols, stages);
-    c.tile = m > 16 ? kTile32 : kTile16;
+    constexpr TileCost few[] = {kCosts[kTile32]};
+    Choice c = pick(few, m, cols, stages);
+    c.tile = kTile32;
     return c;
 }
 
@@ -125,20 +126,12 @@ coc_status product(MmParams p, const Choice& c, hipStream_t stream) {
             else
                 launch_tile<MmTile<T, TA, TB, 2, 2, 2, 4, 3, GATED, false>>(p, c, stream);
             break;
-        case kTile32:
+        default:
             if constexpr (!TA) {
                 if (c.split)
                     launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, true>>(p, c, stream);
                 else
                     launch_tile<MmTile<T, TA, TB, 2, 2, 1, 4, 4, GATED, false>>(p, c, stream);
-            }
-            break;
-        default:
-            if constexpr (!TA) {
-                if (c.split)
-                    launch_tile<MmTile<T, TA, TB, 1, 2, 1, 4, 4, GATED, true>>(p, c, stream);
-                else
-                    launch_tile<MmTile<T, TA, TB, 1, 2, 1, 4, 4, GATED, false>>(p, c, stream);
             }
             break;
     }

@@ -98,10 +98,10 @@ struct Operand {
     static constexpr int STEP = 128 / ES;                             // k of a stage
     static constexpr int BYTES = ROWS * 128;
     static constexpr int INS = BYTES / 1024;                          // load instructions a stage
-    static constexpr int PER_WAVE = INS >= NW ? INS / NW : 1;         // (few: several waves load the same)
+    static constexpr int PER_WAVE = INS / NW;
     static constexpr int CHUNKS = ROWS / 8;                           // TRANS: 16-byte chunks of a k row
     static constexpr int READS = TRANS ? 2 : 1;                       // LDS reads a fragment
-    static_assert(INS % NW == 0 || NW % INS == 0, "loads split over the waves");
+    static_assert(INS % NW == 0, "loads split over the waves");
     static_assert(!TRANS || CHUNKS == 8 || CHUNKS == 16 || CHUNKS == 32, "k rows of 64, 128 or 256 elements");
 
     uint32_t off[PER_WAVE];   // from the stage's base, bytes
@@ -109,7 +109,7 @@ struct Operand {
     const uint8_t* base;
     int64_t step;             // bytes from stage to stage
     uint32_t lds;             // its place in slot 0; NEXT later for each further load
-    static constexpr uint32_t NEXT = INS >= NW ? NW * 1024 : 1024;
+    static constexpr uint32_t NEXT = NW * 1024;
 
     // first(local row or column) -> the global one to read; ld: elements from row to row
     template <class F>
@@ -117,7 +117,7 @@ struct Operand {
                                          F&& first) {
         step = TRANS ? STEP * ld * ES : 128;
         base = (const uint8_t*)p + stage0 * step;
-        q0 = wave % INS * 64 + lane;   // load i of the waves together: neighbouring rows
+        q0 = wave * 64 + lane;   // load i of the waves together: neighbouring rows
 #pragma unroll
         for (int i = 0; i < PER_WAVE; ++i) {
             const int q = q0 + i * NW * 64;
@@ -129,7 +129,7 @@ struct Operand {
                 off[i] = (uint32_t)((int64_t)first(r) * ld * ES) + (uint32_t)c * 16;
             }
         }
-        lds = lds0 + wave % INS * 1024;
+        lds = lds0 + wave * 1024;
     }
     // the k of load i's chunk within its stage
     __device__ __forceinline__ int at(int i) const {

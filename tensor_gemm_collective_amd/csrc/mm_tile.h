@@ -246,7 +246,7 @@ struct MmTile {
             COC_LDS uint8_t* stg = (COC_LDS uint8_t*)sm + wave * (FI * 16 * FJ * 32);
             auto put = [&](auto COLS, auto&& value, uint8_t* c, int64_t ld, int64_t col_of, int col0) {
                 constexpr int NJ = decltype(COLS)::value, PITCH = NJ * 32, CPR = NJ * 2, RPI = 64 / CPR;
-                static_assert(64 % CPR == 0, "staging layout");
+                static_assert(64 % CPR == 0 && FI * 16 % RPI == 0, "staging layout");
 #pragma unroll
                 for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -258,9 +258,8 @@ struct MmTile {
                     }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < (FI * 16 + RPI - 1) / RPI; ++t) {
+                for (int t = 0; t < FI * 16 / RPI; ++t) {
                     const int row = t * RPI + lane / CPR, ch = lane % CPR;
-                    if (FI * 16 % RPI != 0 && row >= FI * 16) continue;
                     const u32x4 v = *(const COC_LDS u32x4*)(stg + row * PITCH + ((ch ^ (row & (CPR - 1))) << 4));
                     const int r = m0 + wm * FI * 16 + row, col = col0 + ch * 8;
                     if (r < p.m && col < p.n) *(u32x4*)(c + (r * ld + col_of + col) * 2) = v;
