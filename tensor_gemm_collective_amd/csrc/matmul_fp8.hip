@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256) void fp8_join(const float* part, T* y, int64_t
     keep_n<4>(y + row * n, col, n, v);
 }
 
-// The tiles, their stages of 128 k timed on products of 100 to 2000 rows.  Tiles of 32 rows
+// The tiles, their stages of 128 k timed on products of 100 to 4000 rows.  Tiles of 32 rows
 // always leave sums to join.  Binary32 results have no tile of 256 x 256: their 16-bit
 // fragments do not fit its registers.
 enum { kTile256, kTile128, kTile64, kTile32, kRows32, kRows16 };
@@ -416,6 +416,12 @@ constexpr TileCost kCosts[] = {
     {64, 128, 2, 0.36f, 0.66f, 1.5f, true, true},
     {32, 128, 2, 0.31f, 0.50f, 1.2f, false, true},
 };
+constexpr TileCost kWideCosts[] = {
+    kCosts[kTile256],   // (not offered)
+    {128, 128, 2, 1.05f, 1.85f, 3.0f, true, true},
+    {64, 128, 2, 0.64f, 1.13f, 2.0f, true, true},
+    {32, 128, 2, 0.49f, 0.85f, 1.5f, false, true},
+};
 
 // Up to 16 rows go straight from memory: 7168 x 8192, bf16, one row 12.1 us (a 16-row tile
 // of split k and its join 14.0; 59 MB, 4.9 TB/s); with 16 weight rows a workgroup every one reads all of x,
@@ -424,19 +430,20 @@ constexpr TileCost kCosts[] = {
 Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
     const int64_t stages = ceil_div(k, kScaleBlock);
     if (m <= 16) return {m <= 4 ? kRows16 : kRows32, 0, 1, false, 0.0f};
+    const TileCost* costs = wide ? kWideCosts : kCosts;
     if (m <= 32) {
-        constexpr TileCost few[] = {kCosts[kTile64], kCosts[kTile32]};
+        const TileCost few[] = {costs[kTile64], costs[kTile32]};
         Choice c = pick(few, m, n, stages);
         c.tile += kTile64;
         return c;
     }
     if (wide) {
-        constexpr TileCost some[] = {kCosts[kTile128], kCosts[kTile64]};
+        const TileCost some[] = {costs[kTile128], costs[kTile64]};
         Choice c = pick(some, m, n, stages);
         c.tile += kTile128;
         return c;
     }
-    constexpr TileCost all[] = {kCosts[kTile256], kCosts[kTile128], kCosts[kTile64]};
+    const TileCost all[] = {costs[kTile256], costs[kTile128], costs[kTile64]};
     return pick(all, m, n, stages);
 }
 

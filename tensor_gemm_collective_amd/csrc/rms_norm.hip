@@ -302,13 +302,15 @@ constexpr int64_t kMaxNorm = 32768;   // elements of a row: 1024 threads of 32
 
 // Workgroups of the backward pass, one part each: a CU's worth, since the parts
 // are written and read again (2048 x 8192 with dsum: 256 workgroups 30.5 us, 512 32.1,
-// 128 36).  Few rows take one, which needs no second kernel nor a workspace (3 x 3084:
-// 10.8 against 13 us, most of it the host's).
+// 128 36).  Few rows take one, which needs no second kernel nor a workspace: up to four a
+// group of threads (16 x 1148 10.5 us with the host's part, 8.8 in a graph; the two kernels 14.9
+// and 6.9; six a group would take 11.4 in a graph), two where a row takes all of a
+// workgroup of 1024 threads (4 x 14336, binary32: 14.8 and 15.4 against 15.0 and 8.0).
 constexpr int64_t kMostParts = 256;
 int64_t backward_parts(int64_t rows, int64_t n) {
     const int64_t groups = n <= 1024 ? 8 : n <= 2048 ? 4 : n <= 4096 ? 2 : 1;   // rows at a time
     const int64_t want = (rows + groups - 1) / groups;
-    return want <= 4 ? 1 : want < kMostParts ? want : kMostParts;
+    return want <= (n <= 8192 ? 4 : 2) ? 1 : want < kMostParts ? want : kMostParts;
 }
 
 template <RowKind K>
