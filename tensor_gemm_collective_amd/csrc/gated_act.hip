@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void gated_forward(const T* gate_up, T* h, uin
     at.col.load(g + f, f, &pu);
     float v[kVec<T>];
 #pragma unroll
-    for (int k = 0; k < kVec<T>; ++k) v[k] = act_value<ACT>(pg.get(k)) * pu.get(k);
+    for (int k = 0; k < kVec<T>; ++k) v[k] = act_of<T, ACT>(pg.get(k)) * pu.get(k);
     o.set(v);
     at.col.store(h + at.row * f, f, o);
 }
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void gated_backward(const T* dh, const T* gate
 #pragma unroll
     for (int k = 0; k < kVec<T>; ++k) {
         float value, slope;
-        act_both<ACT>(pg.get(k), &value, &slope);
+        act_and_slope_of<T, ACT>(pg.get(k), &value, &slope);
         vg[k] = pd.get(k) * pu.get(k) * slope;
         vu[k] = pd.get(k) * value;
     }
