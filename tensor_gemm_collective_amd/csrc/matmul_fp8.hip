@@ -43,9 +43,12 @@ struct Values<true> {
 // 128 k of 16 x 16 outputs.  The 8-bit MFMA adds each lane's products in groups of eight
 // neighbouring k, in which bits below 2^-13 of the largest product's power of two are
 // dropped (measured: a product 2^-13 of another is kept, one of 2^-14 is not, and beyond
-// the group 2^-23 is), and then the groups in binary32: about 2e-5 of the result, a tenth
-// of a rounding to binary16.  Results in binary32 are formed by 16-bit MFMAs, which hold
-// every product whole, at half the rate.
+// the group 2^-23 is), and then the groups in binary32.  A group is off by up to 8 x 2^-13 of
+// its largest product.  Typical of normal data is 2e-5 of the result, a tenth of a rounding
+// to binary16; at worst one 448 x 448 beside seven small products loses them all, 4e-4 of
+// the sum, and where 448 x 448 - 448 x 448 cancels they were the result.  16-bit results are
+// formed so all the same, for twice the rate (4096 x 7168 x 8192: 209 against 415 us);
+// those in binary32 by 16-bit MFMAs, which hold every product whole.
 __device__ __forceinline__ f32x4 mfma_block(const Values<false>& a, const Values<false>& b) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
