@@ -7,7 +7,7 @@ Training, per rank (sequence parallelism: a rank holds tokens / world rows):
 RMS norm with the residual's addition -> all-gather + gate|up matmul -> gated
 activation -> down matmul + reduce-scatter, and the backward pass down to the
 rows, the norm's gamma and the two weights' shards.  With one rank the
-projections and the activation are one kernel (gated_ffn) instead.
+projections and the activation are one call (gated_ffn) instead.
 
 Serving: the weights once in 8 bits, then norm -> product -> activation ->
 product with 8-bit operands, for a prompt or for single tokens.

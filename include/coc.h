@@ -665,15 +665,19 @@ coc_status coc_gated_act_backward(const void* dh, const void* gate_up, void* dga
                                   coc_act act, coc_dtype dt, hipStream_t stream);
 
 /*
- * Both projections, the activation and the product in one kernel:
+ * Both projections, the activation and the product together:
  *
  *   [gate up] = x w,   h = round_dt(act(gate) * up)
+ *
+ * One kernel; or two where its tiles are few (up to some hundred rows): the sums
+ * over d are split and left in ws, and the second adds them and forms h.
  *
  * x: m x d; w: d x 2f, the gate columns and then the up columns (the weight of
  * the column-parallel matmul); h: m x f.  gate_up (optional, m x 2f) receives
  * the rounded projections for the backward pass; h is formed from the
- * unrounded ones.  dt: bf16 or fp16; d and f multiples of 8, m any; pointers
- * 16-byte aligned.  ws: at least coc_gated_ffn_workspace_bytes(m, d, f).
+ * unrounded ones.  dt: bf16 or fp16, subnormal values too count as they are; d
+ * and f multiples of 8, m any; pointers 16-byte aligned.  ws: at least
+ * coc_gated_ffn_workspace_bytes(m, d, f).
  */
 size_t coc_gated_ffn_workspace_bytes(int64_t m, int64_t d, int64_t f);
 coc_status coc_gated_ffn(const void* x, const void* w, void* h, void* gate_up, int64_t m, int64_t d, int64_t f,
@@ -685,10 +689,13 @@ coc_status coc_gated_ffn(const void* x, const void* w, void* h, void* gate_up, i
  *
  *   dx = round_dt([dgate dup] w^T),   dw = round_dt(x^T [dgate dup])
  *
+ * That rounding makes dx and dw about 1.4 times as far off as their own; in fp16
+ * a gradient of a projection below 2^-14 loses bits and one below 2^-25 is lost,
+ * before dw sums over the rows (scale the loss).
  * gate_up (optional): the forward's; where it is NULL the projections are
  * computed again.  dx (m x d) and dw (d x 2f) are optional, either not
- * computed where it is NULL; dw is zeros where m is 0.  ws: at least
- * coc_gated_ffn_backward_workspace_bytes(m, d, f).
+ * computed where it is NULL, the other having the same bits; dw is zeros where
+ * m is 0.  ws: at least coc_gated_ffn_backward_workspace_bytes(m, d, f).
  */
 size_t coc_gated_ffn_backward_workspace_bytes(int64_t m, int64_t d, int64_t f);
 coc_status coc_gated_ffn_backward(const void* dh, const void* x, const void* w, const void* gate_up, void* dx, void* dw,

@@ -153,7 +153,7 @@ def gated_act_backward(dh, gate_up, *, act="silu", dgate_up=None, stream=None):
 
 
 def gated_ffn(x, w, *, act="silu", save=False, h=None, gate_up=None, ws=None, stream=None):
-    """act(gate) * up with [gate up] = x @ w, in one kernel.  x: m x d; w: d x 2f,
+    """act(gate) * up with [gate up] = x @ w, formed together.  x: m x d; w: d x 2f,
     the gate columns and then the up columns.  Returns (h, gate_up); gate_up
     holds the projections where save asks for them or a tensor is given, and is
     None otherwise."""
