@@ -10,7 +10,8 @@ rows, the norm's gamma and the two weights' shards.  With one rank the
 projections and the activation are one call (gated_ffn) instead.
 
 Serving: the weights once in 8 bits, then norm -> product -> activation ->
-product with 8-bit operands, for a prompt or for single tokens.
+product with 8-bit operands, for a prompt or for single tokens; the ranks'
+partial outputs are added.
 """
 import argparse
 import os
@@ -109,6 +110,17 @@ def serve(p, w8, x, residual, act):
     return tgc.matmul_fp8(q, scales, *w8["down"], dtype=x.dtype), total
 
 
+def serve_group(p, w8, x, residual, act):
+    """The block in 8 bits over the ranks, whose weights w8 lists: (output, residual stream).
+    What an all-reduce does over a group of GPUs, the partial outputs' sum, is taken here
+    in binary32 and rounded once."""
+    parts = [serve(p, w, x, residual, act) for w in w8]
+    out = parts[0][0].float()
+    for part, _ in parts[1:]:
+        out = out + part.float()
+    return out.to(x.dtype), parts[0][1]
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     for name, value in (("world", 2), ("tokens", 2048), ("hidden", 1024), ("ffn", 2048), ("steps", 10)):
@@ -123,7 +135,7 @@ def main():
         return [torch.randn(share, a.hidden, generator=g).bfloat16().cuda() for _ in range(a.world)]
 
     x, residual, douts, dsum = rows(), rows(), rows(), rows()
-    w8 = weights_fp8(p)
+    w8 = [weights_fp8(p, r) for r in range(a.world)]
     prompt, token = (torch.randn(n, a.hidden, generator=g).bfloat16().cuda() for n in (a.tokens, 1))
 
     def timed(what, f):
@@ -143,8 +155,9 @@ def main():
         return outs, backward(p, douts, dsum, a.act, saved)
 
     outs, grads = timed(f"step of {a.world} ranks x {share} tokens, hidden {a.hidden}, ffn {a.ffn}", step)
-    timed(f"8 bits, {a.tokens} tokens, one rank's part", lambda: serve(p, w8, prompt, prompt, a.act))
-    timed("8 bits, 1 token, one rank's part", lambda: serve(p, w8, token, token, a.act))
+    for what, t in ((f"{a.tokens} tokens", prompt), ("1 token", token)):
+        timed(f"8 bits, {what}, one rank's part", lambda: serve(p, w8[0], t, t, a.act))
+        timed(f"8 bits, {what}, {a.world} ranks in turn", lambda: serve_group(p, w8, t, t, a.act))
     print(f"|out| {float(torch.stack([o.float().norm() for o in outs]).norm()):.1f}, "
           f"|d rows| {float(torch.stack([d.float().norm() for d in grads['rows']]).norm()):.1f}")
 
