@@ -92,7 +92,7 @@ struct Fp8Tile {
     static constexpr int LATE = HALVES ? A::PER_WAVE / 2 : 0, EARLY = DPW - LATE;   // loads of each part
     static constexpr bool STAGED = !PART && sizeof(T) == 2;   // rows go out through the LDS
     static constexpr int RING = FI >= 4 ? 4 : 2, AHEAD = FI >= 4 ? 2 : 1;   // row fragments held, and read ahead
-    static_assert(FI == 1 || FI % RING == 0, "a block's place is the same in every stage");
+    static_assert(FI % RING == 0, "a block's place is the same in every stage");
     static_assert(BN % kScaleBlock == 0 && kScaleBlock % (FJ * 16) == 0, "a wave's columns share a scale");
     static_assert(XW < NW, "a wave for w's scales");
     static_assert(!STAGED || BM * BN * 2 <= LDS, "the staged output fits in the LDS");

@@ -35,13 +35,11 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
                                                       0, 0);
 }
 
-// Fragment reads of block `j` (16 rows or columns from row0 on), k step ks (32 k).
+// Fragment reads of block `j` (16 rows or columns, counted from init's `first`), k step ks (32 k).
 template <int ROWS, bool TRANS>
 struct Fragments {
     int place[2];
-    int row0;
     __device__ __forceinline__ void init(int first, int lane) {
-        row0 = first;
         if constexpr (TRANS) {
             // a 16-lane group g reads k 8g .. 8g + 3 (then + 4) of its 16 columns: lane
             // 4j + q points at row j's columns 4q, and lane i receives column i
@@ -88,8 +86,6 @@ struct MmParams {
 // p.part for a joining kernel.
 template <class T, bool TA, bool TB, int FI, int FJ, int WM, int WN, int S, bool GATED, bool PART>
 struct MmTile {
-    using Type = T;
-    static constexpr bool SPLIT = PART;
     static constexpr int NW = WM * WN, BM = WM * FI * 16, BN = WN * FJ * 16;
     static constexpr int OUT = GATED ? BN / 2 : BN;   // columns of C a tile gives
     using A = Operand<BM, TA, NW>;
