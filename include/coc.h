@@ -587,7 +587,9 @@ coc_status coc_moe_combine_backward(const void* dy, const void* h, const int32_t
  * x, y, residual, sum_out: rows x n of `dt`, element-aligned; gamma: n of
  * `param_dt` (dt or COC_F32); rstd: rows, binary32.  residual is optional;
  * where it is given sum_out receives h (the next residual, and the x of the
- * backward pass), otherwise sum_out is not used.
+ * backward pass), otherwise sum_out is not used.  The squares are summed as they
+ * are: |h| from 2^56 on may overflow (y is then 0), and with eps = 0 rows below
+ * 2^-60 underflow.
  */
 coc_status coc_rms_norm(const void* x, const void* residual, const void* gamma, void* y, void* sum_out, float* rstd,
                         int64_t rows, int64_t n, float eps, coc_dtype dt, coc_dtype param_dt, hipStream_t stream);

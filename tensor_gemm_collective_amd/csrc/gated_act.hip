@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void gated_forward(const T* gate_up, T* h, uin
 }
 
 // dg = dh u act'(g), du = dh act(g).  Memory bound, three reads and two writes: 4096 x 3584
-// (bf16, 147 MB) 28 us, 5.2 TB/s.
+// (bf16, 147 MB) 21.8 us by itself, 28 (5.2 TB/s) in front of the products of gated_ffn's gradient.
 template <class T, int ACT, RowKind KIND>
 __global__ __launch_bounds__(256) void gated_backward(const T* dh, const T* gate_up, T* dgate_up, uint32_t vectors,
                                                       uint32_t per_row, int f) {

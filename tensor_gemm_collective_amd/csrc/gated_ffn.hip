@@ -68,11 +68,11 @@ __global__ __launch_bounds__(256) void fill_zeros(T* p, int64_t vectors) {
 // its operands least often.  128 x 128 comes with four slots, one workgroup a CU, for
 // products of few tiles, and with two slots and two workgroups a CU.
 //
-// The small tiles wait for their loads (24 KB a stage of 64 x 128): six slots for three, waves
-// that share a stage's k and read a third less from the LDS, half the LDS reads, no barriers and
-// loads that keep their lines in the L1 all took the same time (non-temporal ones up to 1.8 times
-// it); on a copy whose loads all hit the L2 1024 x 2048 x 4096 took 27 of 28 us, 3313 x 304 x
-// 4056 24 of 29 and 128 x 7168 x 8192, unsplit, 41 of 81; with no loads 17, 16 and 27.
+// What the small tiles (24 KB a stage of 64 x 128) are bound by is not one thing: six slots for
+// three, waves that share a stage's k and read a third less from the LDS, half the LDS reads, no
+// barriers and loads that keep their lines in the L1 all took the same time (non-temporal ones up
+// to 1.8 times it); on a copy whose loads all hit the L2 1024 x 2048 x 4096 took 27 of 28 us, 3313
+// x 304 x 4056 24 of 29 and 128 x 7168 x 8192, unsplit, 41 of 81; with no loads 17, 16 and 27.
 enum { kTile256, kTile128Deep, kTile128, kTile64, kTile32 };
 constexpr TileCost kCosts[] = {
     {256, 256, 1, 1.35f, 1.50f, 6.0f, true, false}, {128, 128, 1, 0.55f, 0.55f, 3.0f, true, false},
